@@ -61,6 +61,7 @@ enum {
 /* Activations ("Code Walkthrough - SER", gating / routing path: ReLU, GELU, Swish).
  * GELU is the exact form 0.5 z (1 + erf(z / sqrt 2)); Swish is z * sigmoid(z). */
 enum { MOE_ACT_RELU = 0, MOE_ACT_GELU = 1, MOE_ACT_SWISH = 2 };
+enum { MOE_ACT_NONE = -1 }; /* moe_mx_gemm only */
 
 /* Top-k methods (same page, "Configuration"): GREEDY selects the highest logits;
  * NOISY adds caller-supplied noise to the logits before selection. */
@@ -368,6 +369,135 @@ MOE_API size_t moe_ep_experts_workspace_bytes(const moe_layer_t *layer, int32_t 
 MOE_API int moe_ep_experts(moe_layer_t *layer, const void *recv_x, const int32_t *recv_rows, int32_t R,
                            void *recv_out, void *workspace, size_t ws_bytes, void *stream);
 MOE_API int moe_ep_combine(moe_layer_t *layer, void *y, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Routing from given logits, and its gradient. Stands beside the layer's own
+ * router for models whose routing is not the renormalised softmax of it: the
+ * logits come from the caller (a router product of their own, or the logits of
+ * moe_forward). For each token with logits l:
+ *   s = softmax(l) or sigmoid(l);
+ *   key_e = s_e + bias_e; without bias s_e (with groups) or l_e (without);
+ *   groups (num_groups > 1): experts g E/num_groups .. are group g, its score is
+ *   the sum of its group_top highest keys, and only the experts of the
+ *   top_groups best groups can be selected;
+ *   the num_active highest keys are selected, by descending key;
+ *   w_r = scale * s_e(r) / (sum over the selection of s), without the division
+ *   when renormalize is 0. The bias ("Balancing": b_i) takes no part in w.
+ * Equal keys go to the lower expert, equal group scores to the lower group. The
+ * selection is the one of keys computed in 64 bits.
+ * An expert whose logit is -inf or NaN, or whose key is, is never selected; where
+ * fewer than num_active experts are left, the remaining choices have index -1 and
+ * weight 0. A logit of +inf gives unspecified weights and valid indices. */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+
+typedef struct {
+    int32_t num_experts; /* E, 1..512                                               */
+    int32_t num_active;  /* k, 1..min(E, 32), at most top_groups E / num_groups     */
+    int32_t score;       /* MOE_SCORE_*                                             */
+    int32_t num_groups;  /* divides E, 1..32; 1 = no groups                         */
+    int32_t top_groups;  /* 1..num_groups                                           */
+    int32_t group_top;   /* keys that make a group's score, 1 or 2                  */
+    int32_t renormalize; /* 1: the weights of a token sum to scale                  */
+    float scale;
+    int32_t dtype;       /* MOE_DTYPE_* of the logits and of their gradient         */
+} moe_route_config_t;
+
+/* E=8, k=2, softmax, no groups (group_top 2), renormalised, scale 1, FP32 logits. */
+MOE_API moe_route_config_t moe_route_config_default(void);
+
+/* Routes T >= 0 tokens.
+ *   logits   [T] rows of E elements, `ld` elements apart (ld >= E; aligned to an element)
+ *   bias     [E] fp32 or NULL
+ *   weights  [T][k] fp32, topk_idx [T][k] int32
+ *   counts   [E] int32 selections per expert, or NULL
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+MOE_API int moe_route(const moe_route_config_t *cfg, const void *logits, int64_t ld, int32_t T, const float *bias,
+                      float *weights, int32_t *topk_idx, int32_t *counts, void *stream);
+
+/* Gradient of moe_route's weights with respect to the logits: given
+ * grad_weights [T][k] fp32 (dL/dw) and the forward's logits and topk_idx, writes
+ * every element of grad_logits [T] x E (rows grad_ld apart, the logits' type; may
+ * not overlap logits). The selection is constant and the bias has no gradient.
+ *   renormalised: dL/ds_r = scale / S (g_r - sum_j g_j s_j / S), S = sum_j s_j;
+ *   otherwise:    dL/ds_r = scale g_r;
+ * then through s: s (1 - s) for the sigmoid, the softmax's Jacobian otherwise.
+ * An index outside 0..E-1 (the -1 of a missing choice) counts as absent; one that
+ * appears twice adds up. Sums are fp32; bf16 gradients are rounded once. */
+MOE_API int moe_route_backward(const moe_route_config_t *cfg, const float *grad_weights, const void *logits, int64_t ld,
+                               const int32_t *topk_idx, int32_t T, void *grad_logits, int64_t grad_ld, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Microscaled 4-bit floating point: rows of E2M1 codes (magnitudes 0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6) with one scale per block of neighbouring elements.
+ *   MXFP4: blocks of 32, scales powers of two (E8M0): 2^(floor(log2 max) - 2);
+ *   NVFP4: blocks of 16, E4M3 scales: max / 6, rounded to nearest even, at most 448.
+ * Every element becomes the nearest code times its scale (ties to the even code,
+ * magnitudes above 6 scales to 6). scale_exp e takes a power of two out of the
+ * whole matrix first: x 2^-e is quantised, and the values count 2^e. (NVFP4's
+ * scales reach from 2^-9 to 448; MXFP4 needs no e.) A block with an infinity or
+ * a NaN has the value NaN; one whose NVFP4 scale rounds to 0 the value 0.
+ * Layout of `rows` x `cols` (cols a multiple of 32):
+ *   codes   [rows][cols / 2] bytes, the even column in the low four bits;
+ *   scales  tiles of 128 rows x 4 blocks, 512 bytes each: the byte of row r and
+ *           block j is at (r / 128 * SB + j / 4) * 512 + (r % 32) * 16
+ *           + (r % 128 / 32) * 4 + j % 4, SB = ceil(blocks per row / 4);
+ *           blocks past the row's end hold 0, rows past `rows` anything.
+ * Both 16-byte aligned. moe_mx_codes_bytes and moe_mx_scales_bytes give the
+ * sizes (0 for arguments that are not valid). */
+enum { MOE_MX_MXFP4 = 0, MOE_MX_NVFP4 = 1 };
+
+MOE_API size_t moe_mx_codes_bytes(int64_t rows, int64_t cols);
+MOE_API size_t moe_mx_scales_bytes(int32_t format, int64_t rows, int64_t cols);
+
+/* Quantises rows of x (dtype MOE_DTYPE_*, rows `ld` elements apart, x_rows of them).
+ *   row_index  [rows] int32: output row r is x's row row_index[r]; where that is
+ *              outside 0..x_rows-1 row r of every output is left as it was.
+ *              NULL: row r is x's row r (rows must equal x_rows)
+ *   values     optional [rows] rows of cols, values_ld apart, in x's type: what
+ *              codes and scales stand for (exact in both types, as long as it is in
+ *              the type's range)
+ * scale_exp in -60..60. Errors: INVALID_ARG, CUDA. */
+MOE_API int moe_mx_quantize(int32_t format, const void *x, int32_t dtype, int64_t ld, int32_t x_rows, int32_t cols,
+                            const int32_t *row_index, int32_t rows, int32_t scale_exp, void *codes, void *scales,
+                            void *values, int64_t values_ld, void *stream);
+
+/* The values of codes and scales, to `out` (dtype MOE_DTYPE_*, rows ld apart). */
+MOE_API int moe_mx_dequantize(int32_t format, const void *codes, const void *scales, int32_t rows, int32_t cols,
+                              int32_t scale_exp, void *out, int32_t dtype, int64_t ld, void *stream);
+
+/* Grouped product of 4-bit rows with 4-bit weights, on the block-scaled tensor
+ * cores (stands beside moe_ep_experts, whose experts are bf16):
+ *   out[r][j] = act(alpha[g] 2^scale_exp sum_i A[r][i] W[g][j][i] + bias[g][j])
+ * for the rows r of every group g, summed in fp32 and rounded once.
+ *   a_codes, a_scales  rows x k, as moe_mx_quantize writes them
+ *   w_codes            [groups][n][k / 2]; w_scales: the scale tiles of every
+ *                      group's n x k matrix, one after another (each
+ *                      moe_mx_scales_bytes(format, n, k) bytes)
+ *   group_start, group_rows  device int32 [groups]: group g has rows
+ *                      group_start[g] .. + group_rows[g] - 1 of A and out; starts
+ *                      are multiples of 128, segments do not overlap and end within
+ *                      `rows`. Both NULL (groups = 1): all rows are group 0.
+ *                      Other rows of out are left as they were. A segment that
+ *                      breaks these bounds is not computed, and sets bit 1 of *status
+ *   bias               [groups][n] fp32 or NULL; alpha [groups] fp32 or NULL (1)
+ *   scale_exp          -120..120, the sum of both operands' exponents
+ *   activation         MOE_ACT_*, MOE_ACT_NONE = none
+ *   out                rows of n, out_ld apart, out_dtype MOE_DTYPE_*
+ *   status             device word or NULL: bits are or-ed in (bit 0: a bounded
+ *                      wait gave up, out is incomplete; bit 1 as above)
+ * groups <= 1024, groups x n < 2^31. rows = 0 enqueues nothing. Needs no
+ * workspace; calls on any streams may overlap. Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+typedef struct {
+    int32_t format, rows, n, k, groups;
+    int32_t scale_exp, activation, out_dtype;
+    int64_t out_ld;
+    const void *a_codes, *a_scales, *w_codes, *w_scales;
+    const int32_t *group_start, *group_rows;
+    const float *bias, *alpha;
+    void *out;
+    uint32_t *status;
+} moe_mx_gemm_t;
+MOE_API int moe_mx_gemm(const moe_mx_gemm_t *args, void *stream);
 
 /* Self-check of the bounded waits the tcgen05 kernels rely on (no counterpart
  * on the pages): one GPU thread waits on an mbarrier that nothing arrives on;

@@ -20,6 +20,9 @@ MOE_TOPK = {"greedy": 0, "noisy": 1}
 MOE_DTYPE = {"bf16": 0, "fp32": 1}
 MOE_CREDIT = {"output": 0, "hidden": 1}
 MOE_PRIORITY = {"token": 0, "rank": 1}
+MOE_ACT_NONE = -1
+MOE_SCORE = {"softmax": 0, "sigmoid": 1}
+MOE_MX = {"mxfp4": 0, "nvfp4": 1}
 
 # Every symbol include/moe.h declares.
 EXPORTS = ("moe_config_default", "moe_layer_create", "moe_workspace_bytes", "moe_capacity", "moe_forward",
@@ -27,7 +30,8 @@ EXPORTS = ("moe_config_default", "moe_layer_create", "moe_workspace_bytes", "moe
            "moe_update_selection_bias", "moe_dro_update", "moe_selftest_bounded_wait", "moe_selftest_gemm_timeout",
            "moe_selftest_router_timeout", "moe_router_planes_bytes", "moe_prepare_router",
            "moe_ep_dispatch", "moe_ep_layout", "moe_ep_experts_workspace_bytes", "moe_ep_experts", "moe_ep_combine", "moe_device_status", "moe_set_timing_events", "moe_launch_count", "moe_destroy", "moe_status_string",
-           "moe_last_error")
+           "moe_last_error", "moe_route_config_default", "moe_route", "moe_route_backward", "moe_mx_codes_bytes",
+           "moe_mx_scales_bytes", "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_gemm")
 
 
 class MoeConfig(ctypes.Structure):
@@ -57,6 +61,21 @@ class MoeStats(ctypes.Structure):
                 ("l_z", ctypes.c_void_p), ("n_dropped", ctypes.c_void_p), ("credit", ctypes.c_void_p),
                 ("expert_loss", ctypes.c_void_p), ("importance", ctypes.c_void_p), ("cv_load", ctypes.c_void_p),
                 ("cv_importance", ctypes.c_void_p), ("l_total", ctypes.c_void_p)]
+
+
+class MoeRouteConfig(ctypes.Structure):
+    _fields_ = [("num_experts", ctypes.c_int32), ("num_active", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("num_groups", ctypes.c_int32), ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
+class MoeMxGemm(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("rows", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("scale_exp", ctypes.c_int32), ("activation", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("out_ld", ctypes.c_int64), ("a_codes", ctypes.c_void_p),
+                ("a_scales", ctypes.c_void_p), ("w_codes", ctypes.c_void_p), ("w_scales", ctypes.c_void_p),
+                ("group_start", ctypes.c_void_p), ("group_rows", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("alpha", ctypes.c_void_p), ("out", ctypes.c_void_p), ("status", ctypes.c_void_p)]
 
 
 class MoEError(RuntimeError):
@@ -130,6 +149,22 @@ def lib() -> ctypes.CDLL:
         L.moe_status_string.argtypes = [ctypes.c_int]
         L.moe_last_error.restype = ctypes.c_char_p
         L.moe_last_error.argtypes = []
+        L.moe_route_config_default.restype = MoeRouteConfig
+        L.moe_route_config_default.argtypes = []
+        L.moe_route.restype = ctypes.c_int
+        L.moe_route.argtypes = [ctypes.POINTER(MoeRouteConfig), vp, i64, i32, vp, vp, vp, vp, vp]
+        L.moe_route_backward.restype = ctypes.c_int
+        L.moe_route_backward.argtypes = [ctypes.POINTER(MoeRouteConfig), vp, vp, i64, vp, i32, vp, i64, vp]
+        L.moe_mx_codes_bytes.restype = sz
+        L.moe_mx_codes_bytes.argtypes = [i64, i64]
+        L.moe_mx_scales_bytes.restype = sz
+        L.moe_mx_scales_bytes.argtypes = [i32, i64, i64]
+        L.moe_mx_quantize.restype = ctypes.c_int
+        L.moe_mx_quantize.argtypes = [i32, vp, i32, i64, i32, i32, vp, i32, i32, vp, vp, vp, i64, vp]
+        L.moe_mx_dequantize.restype = ctypes.c_int
+        L.moe_mx_dequantize.argtypes = [i32, vp, vp, i32, i32, i32, vp, i32, i64, vp]
+        L.moe_mx_gemm.restype = ctypes.c_int
+        L.moe_mx_gemm.argtypes = [ctypes.POINTER(MoeMxGemm), vp]
         _lib = L
     return _lib
 
@@ -245,6 +280,47 @@ def moe_selftest_router_timeout(layer: int, x: int, T: int, workspace: int, ws_b
 
 def moe_device_status(layer: int, stream: int) -> int:
     return int(lib().moe_device_status(layer, stream))
+
+
+def moe_route_config_default() -> MoeRouteConfig:
+    return lib().moe_route_config_default()
+
+
+def moe_route(cfg: MoeRouteConfig, logits: Optional[int], ld: int, T: int, bias: Optional[int], weights: Optional[int],
+              topk_idx: Optional[int], counts: Optional[int], stream: int) -> int:
+    return _check(lib().moe_route(ctypes.byref(cfg), logits, ld, T, bias, weights, topk_idx, counts, stream),
+                  "moe_route")
+
+
+def moe_route_backward(cfg: MoeRouteConfig, grad_weights: Optional[int], logits: Optional[int], ld: int,
+                       topk_idx: Optional[int], T: int, grad_logits: Optional[int], grad_ld: int, stream: int) -> int:
+    return _check(lib().moe_route_backward(ctypes.byref(cfg), grad_weights, logits, ld, topk_idx, T, grad_logits,
+                                           grad_ld, stream), "moe_route_backward")
+
+
+def moe_mx_codes_bytes(rows: int, cols: int) -> int:
+    return int(lib().moe_mx_codes_bytes(rows, cols))
+
+
+def moe_mx_scales_bytes(fmt: int, rows: int, cols: int) -> int:
+    return int(lib().moe_mx_scales_bytes(fmt, rows, cols))
+
+
+def moe_mx_quantize(fmt: int, x: Optional[int], dtype: int, ld: int, x_rows: int, cols: int, row_index: Optional[int],
+                    rows: int, scale_exp: int, codes: Optional[int], scales: Optional[int], values: Optional[int],
+                    values_ld: int, stream: int) -> int:
+    return _check(lib().moe_mx_quantize(fmt, x, dtype, ld, x_rows, cols, row_index, rows, scale_exp, codes, scales,
+                                        values, values_ld, stream), "moe_mx_quantize")
+
+
+def moe_mx_dequantize(fmt: int, codes: Optional[int], scales: Optional[int], rows: int, cols: int, scale_exp: int,
+                      out: Optional[int], dtype: int, ld: int, stream: int) -> int:
+    return _check(lib().moe_mx_dequantize(fmt, codes, scales, rows, cols, scale_exp, out, dtype, ld, stream),
+                  "moe_mx_dequantize")
+
+
+def moe_mx_gemm(args: MoeMxGemm, stream: int) -> int:
+    return _check(lib().moe_mx_gemm(ctypes.byref(args), stream), "moe_mx_gemm")
 
 
 MOE_TIMING_EVENTS = 8

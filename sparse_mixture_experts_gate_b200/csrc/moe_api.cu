@@ -100,6 +100,20 @@ namespace moe {
 // Records `msg` as the calling thread's last error (for moe_last_error) and
 // returns `code`; used by entry points defined in other files.
 int report_error(int code, const char *msg) { return fail(code, "%s", msg); }
+
+// Row-major bytes [rows][inner] read in boxes of 128 x box_rows with 128B
+// swizzle (4-bit codes as K-major operands).
+bool encode_u8_2d(CUtensorMap *m, const void *base, uint64_t inner, uint64_t rows, uint32_t box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn || rows == 0) return false;
+    cuuint64_t dims[2] = {inner, rows};
+    cuuint64_t strides[1] = {inner};
+    cuuint32_t box[2] = {128, box_rows};
+    cuuint32_t es[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 }  // namespace moe
 
 struct moe_layer {

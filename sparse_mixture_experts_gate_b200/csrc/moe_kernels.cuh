@@ -303,4 +303,8 @@ cudaError_t launch_bias_update(const BiasUpdateArgs &a, cudaStream_t s, int *lau
 // Sets the calling thread's last-error message; returns `code`.
 int report_error(int code, const char *msg);
 
+// Tensor map of row-major bytes [rows][inner] (inner a multiple of 16): boxes
+// of 128 bytes x box_rows, 128B swizzle.
+bool encode_u8_2d(CUtensorMap *m, const void *base, uint64_t inner, uint64_t rows, uint32_t box_rows);
+
 }  // namespace moe

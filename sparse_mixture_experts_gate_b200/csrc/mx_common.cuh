@@ -1,0 +1,148 @@
+// mx_common.cuh - the microscaled 4-bit formats: argument blocks, scale layout
+// and the tcgen05 wrappers of block-scaled products.
+//
+// A row of cols elements is stored as cols / 2 bytes of E2M1 codes (two in a
+// byte, the even column in the low four bits; magnitudes 0, 0.5, 1, 1.5, 2, 3,
+// 4, 6, the sign in bit 3) and one scale byte per block:
+//   MXFP4: blocks of 32, E8M0 scales 2^(byte - 127), 255 = NaN;
+//   NVFP4: blocks of 16, E4M3 scales, times one power of two for the tensor.
+// Scale bytes lie in tiles of 128 rows x 4 blocks, 512 bytes each, which is the
+// order tcgen05.cp copies into TMEM: the byte of (row r, block j) is at
+//   (r / 128 * SB + j / 4) * 512 + (r % 32) * 16 + (r % 128 / 32) * 4 + j % 4,
+// SB = ceil(blocks per row / 4); the bytes of blocks past the row's end are 0.
+#pragma once
+
+#include "moe_common.cuh"
+
+namespace moe {
+
+enum { kMxFp4 = 0, kNvFp4 = 1 };
+
+template <int FMT>
+struct MxFormat {
+    static constexpr int kBlock = FMT == kMxFp4 ? 32 : 16;  // elements per scale
+    static constexpr int kTileK = 4 * kBlock;               // elements of K per 512-byte scale tile
+};
+
+__host__ __device__ __forceinline__ int mx_scale_tiles(int cols, int block) {
+    return (cols + 4 * block - 1) / (4 * block);
+}
+
+struct MxQuantArgs {
+    const void *x;             // [x_rows][ld] bf16 or fp32
+    int64_t ld;
+    int x_rows;
+    const int32_t *row_index;  // [rows] source row of each output row (others are skipped), or null
+    int rows, cols;
+    float pre;                 // 2^-scale_exp
+    uint8_t *codes;            // [rows][cols / 2]
+    uint8_t *scales;           // tiles
+    void *values;              // [rows][values_ld] in x's type, or null
+    int64_t values_ld;
+    float post;                // 2^scale_exp
+};
+cudaError_t launch_mx_quantize(const MxQuantArgs &a, int format, bool bf16, cudaStream_t s);
+
+struct MxDequantArgs {
+    const uint8_t *codes, *scales;
+    int rows, cols;
+    float post;
+    void *out;
+    int64_t ld;
+};
+cudaError_t launch_mx_dequantize(const MxDequantArgs &a, int format, bool bf16, cudaStream_t s);
+
+struct MxGemmArgs {
+    const uint8_t *a_scales, *w_scales;
+    const int32_t *group_start, *group_rows;  // [G] or null (one group of all rows)
+    int rows, N, K, G;
+    const float *bias;   // [G][N] or null
+    const float *alpha;  // [G] or null
+    float post;          // 2^scale_exp of both operands
+    int act;             // activation code, -1 none
+    void *out;
+    int out_f32;
+    int64_t out_ld;
+    int wide_ok;         // out and out_ld allow 4-byte stores of bf16 pairs
+    uint32_t *status;    // or null
+};
+cudaError_t launch_mx_gemm(const CUtensorMap &map_w, const CUtensorMap &map_a, const MxGemmArgs &a, int format,
+                           int num_sms, cudaStream_t s);
+
+// Device status bits the product adds to kDevTimeout.
+enum : uint32_t { kDevBadGroup = 2u };
+
+// ------------------------------------------------------------------ tcgen05
+
+// Shared-memory descriptor of one 512-byte scale tile (32 rows of 16 bytes, no
+// swizzle, 8-row groups 128 bytes apart) for tcgen05.cp.32x128b.
+__device__ __forceinline__ uint64_t scale_tile_desc(uint32_t smem_addr) {
+    return static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 16) |
+           (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+
+// Copies a scale tile into 4 TMEM columns (32 lanes, repeated in the four lane
+// quarters). Executes in order with the MMAs this thread issues after it.
+template <int CG>
+__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t desc) {
+    if constexpr (CG == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Instruction descriptor of kind::mxf4 / kind::mxf4nvf4 with E2M1 operands,
+// fp32 accumulation, K-major, shape M x N x 64: B scale id in [4,6), A format
+// in [7,10) and B format in [10,12) (1 = E2M1), N >> 3 in [17,23), scale type
+// in bit 23 (1 = UE8M0, 0 = UE4M3), M >> 7 in [27,29), A scale id in [29,31).
+// The scale ids are or-ed in (mx_idesc_sf): which bytes of the 4-byte scale
+// words the MMA uses.
+template <int FMT>
+__host__ __device__ constexpr uint32_t mx_idesc(int M, int N) {
+    return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | ((FMT == kMxFp4 ? 1u : 0u) << 23) |
+           (static_cast<uint32_t>(M >> 7) << 27);
+}
+__host__ __device__ constexpr uint32_t mx_idesc_sf(uint32_t id) { return (id << 4) | (id << 29); }
+
+// D[tmem] (+)= (A * scale_a) (B * scale_b)^T over 64 elements of K.
+template <int FMT, int CG>
+__device__ __forceinline__ void tc_mma_mx(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+#define MOE_MX_MMA(KIND, CGS, VEC)                                                                            \
+    asm volatile(                                                                                             \
+        "{\n\t.reg .pred p;\n\t"                                                                              \
+        "setp.ne.b32 p, %6, 0;\n\t"                                                                           \
+        "tcgen05.mma.cta_group::" CGS ".kind::" KIND ".block_scale.scale_vec::" VEC                           \
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),                                               \
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)                             \
+        : "memory")
+    if constexpr (FMT == kMxFp4 && CG == 1) MOE_MX_MMA("mxf4", "1", "2X");
+    if constexpr (FMT == kMxFp4 && CG == 2) MOE_MX_MMA("mxf4", "2", "2X");
+    if constexpr (FMT == kNvFp4 && CG == 1) MOE_MX_MMA("mxf4nvf4", "1", "4X");
+    if constexpr (FMT == kNvFp4 && CG == 2) MOE_MX_MMA("mxf4nvf4", "2", "4X");
+#undef MOE_MX_MMA
+}
+
+// Untiled bulk copy into shared memory (16-byte aligned addresses and size),
+// completing on `bar`.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// The value of an E4M3 byte (0x7f and 0xff are NaN).
+__device__ __forceinline__ float e4m3_value(uint32_t b) {
+    const uint32_t e = (b >> 3) & 15u, m = b & 7u;
+    if ((b & 0x7fu) == 0x7fu) return __uint_as_float(0x7fffffffu);
+    return e ? __uint_as_float(((e + 120u) << 23) | (m << 20)) : static_cast<float>(m) * 0.001953125f;
+}
+
+// The value of an E8M0 byte.
+__device__ __forceinline__ float e8m0_value(uint32_t b) {
+    if (b == 255u) return __uint_as_float(0x7fffffffu);
+    return b ? __uint_as_float(b << 23) : __uint_as_float(1u << 22);
+}
+
+}  // namespace moe

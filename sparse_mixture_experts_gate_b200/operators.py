@@ -1,0 +1,214 @@
+"""The operators of libmoe.so that need no layer, on torch tensors.
+
+Routing to experts from given logits and its gradient (`route`, `route_backward`),
+and microscaled 4-bit floating point: rows of codes and scales (`MxTensor`), made by
+`mx_quantize`, read back by `mx_dequantize`, and multiplied with 4-bit expert
+weights by `mx_gemm`. Checks and pointer marshalling only; the work is done by the
+kernels behind the C ABI (include/moe.h has the definitions). Every call runs on the
+current stream of its tensors' device; nothing is differentiable through autograd.
+"""
+from __future__ import annotations
+
+from typing import Optional, Tuple
+
+import torch
+
+from . import binding as B
+
+_DTYPE = {torch.bfloat16: 0, torch.float32: 1}
+_BLOCK = {"mxfp4": 32, "nvfp4": 16}
+
+
+def _ptr(t) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _on(t: torch.Tensor):
+    """The raw current stream of t's device; the call has to run with that device current."""
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _call(t: torch.Tensor, fn, *args):
+    """fn(*args, stream) with t's device current."""
+    if not t.is_cuda:
+        raise ValueError("the operators take CUDA tensors")
+    if t.device.index == torch.cuda.current_device():
+        return fn(*args, _on(t))
+    with torch.cuda.device(t.device):
+        return fn(*args, _on(t))
+
+
+def _rows(name: str, t: torch.Tensor, cols: Optional[int] = None) -> int:
+    """The row stride of a matrix whose rows are contiguous."""
+    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name}: a matrix{'' if cols is None else f' of {cols} columns'} is needed, "
+                         f"got {tuple(t.shape)}")
+    if t.dtype not in _DTYPE:
+        raise ValueError(f"{name}: bf16 or fp32, got {t.dtype}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows have to be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _array(name: str, t: Optional[torch.Tensor], like: torch.Tensor, dtype, shape=None):
+    if t is None:
+        return
+    if t.dtype != dtype or not t.is_contiguous() or t.device != like.device or \
+            (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name}: a contiguous {dtype} tensor{'' if shape is None else f' of {tuple(shape)}'} on "
+                         f"{like.device} is needed, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+class RouteConfig:
+    """How tokens are routed: `score` "softmax" or "sigmoid"; with num_groups > 1 only the
+    experts of the top_groups best groups (by the sum of their group_top highest keys);
+    weights renormalised over the selection or not, times `scale`."""
+
+    def __init__(self, num_experts: int, num_active: int, score: str = "softmax", num_groups: int = 1,
+                 top_groups: int = 1, group_top: int = 2, renormalize: bool = True, scale: float = 1.0):
+        if score not in B.MOE_SCORE:
+            raise ValueError(f"unknown score {score!r}")
+        self.num_experts, self.num_active = num_experts, num_active
+        self._c = {d: B.MoeRouteConfig(num_experts, num_active, B.MOE_SCORE[score], num_groups, top_groups, group_top,
+                                       int(renormalize), scale, code) for d, code in _DTYPE.items()}
+
+
+def route(logits: torch.Tensor, cfg: RouteConfig, bias: Optional[torch.Tensor] = None, counts: bool = True,
+          out=None) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
+    """Routes the tokens of logits [T][E] (bf16 or fp32). Returns (weights [T][k] fp32,
+    topk_idx [T][k] int32, selections per expert [E] int32 or None); `out`: these
+    three to write into. bias [E] fp32 takes part in the selection only."""
+    ld = _rows("logits", logits, cfg.num_experts)
+    T, E, k = logits.shape[0], cfg.num_experts, cfg.num_active
+    if bias is not None:
+        _array("bias", bias, logits, torch.float32, (E,))
+    if out is None:
+        w = torch.empty(T, k, dtype=torch.float32, device=logits.device)
+        idx = torch.empty(T, k, dtype=torch.int32, device=logits.device)
+        n = torch.empty(E, dtype=torch.int32, device=logits.device) if counts else None
+    else:
+        w, idx, n = out
+        _array("weights", w, logits, torch.float32, (T, k))
+        _array("topk_idx", idx, logits, torch.int32, (T, k))
+        _array("counts", n, logits, torch.int32, (E,))
+    _call(logits, B.moe_route, cfg._c[logits.dtype], _ptr(logits), ld, T, _ptr(bias), _ptr(w), _ptr(idx), _ptr(n))
+    return w, idx, n
+
+
+def route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, topk_idx: torch.Tensor, cfg: RouteConfig,
+                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient with respect to logits, given that of route's weights [T][k] fp32."""
+    ld = _rows("logits", logits, cfg.num_experts)
+    T, k = logits.shape[0], cfg.num_active
+    _array("grad_weights", grad_weights, logits, torch.float32, (T, k))
+    _array("topk_idx", topk_idx, logits, torch.int32, (T, k))
+    if out is None:
+        out = torch.empty(T, cfg.num_experts, dtype=logits.dtype, device=logits.device)
+    elif out.dtype != logits.dtype or out.shape != logits.shape or out.device != logits.device:
+        raise ValueError("out has to be like logits")
+    _call(logits, B.moe_route_backward, cfg._c[logits.dtype], _ptr(grad_weights), _ptr(logits), ld, _ptr(topk_idx), T,
+          _ptr(out), _rows("out", out))
+    return out
+
+
+class MxTensor:
+    """Rows of microscaled 4-bit floating point: `groups` matrices of rows x cols ("mxfp4" or
+    "nvfp4"), codes [groups * rows][cols / 2] and scale tiles as uint8 tensors on one device,
+    and the power of two scale_exp that the values count in."""
+
+    def __init__(self, fmt: str, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int, groups: int = 1,
+                 scale_exp: int = 0):
+        if fmt not in B.MOE_MX:
+            raise ValueError(f"unknown format {fmt!r}")
+        if cols < 32 or cols % 32:
+            raise ValueError(f"a row needs a positive multiple of 32 elements, got {cols}")
+        for name, t, need in (("codes", codes, groups * B.moe_mx_codes_bytes(rows, cols)),
+                              ("scales", scales, groups * B.moe_mx_scales_bytes(B.MOE_MX[fmt], rows, cols))):
+            if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() < need or t.device != codes.device:
+                raise ValueError(f"{name}: at least {need} contiguous bytes on one device are needed")
+        self.format, self.codes, self.scales = fmt, codes, scales
+        self.rows, self.cols, self.groups, self.scale_exp = rows, cols, groups, scale_exp
+
+
+def mx_tile_scales(scales: torch.Tensor) -> torch.Tensor:
+    """Scale bytes [groups][rows][blocks] (a checkpoint's plain order) as scale tiles."""
+    G, N, S = scales.shape
+    nb, sb = -(-N // 128), -(-S // 4)
+    p = torch.zeros(G, nb * 128, sb * 4, dtype=torch.uint8, device=scales.device)
+    p[:, :N, :S] = scales
+    return p.view(G, nb, 4, 32, sb, 4).permute(0, 1, 4, 3, 2, 5).contiguous()
+
+
+def mx_quantize(x: torch.Tensor, fmt: str = "mxfp4", row_index: Optional[torch.Tensor] = None, scale_exp: int = 0,
+                values: Optional[torch.Tensor] = None, out: Optional[MxTensor] = None) -> MxTensor:
+    """Rows of x (bf16 or fp32) to 4 bits. row_index [rows] int32: output row r is x's row
+    row_index[r], and is left as it was where that is no row of x. `values`, in x's type,
+    receives what the codes stand for; `out`: an MxTensor to write into."""
+    ld = _rows("x", x)
+    rows, cols = (x.shape[0] if row_index is None else row_index.numel()), x.shape[1]
+    _array("row_index", row_index, x, torch.int32)
+    if fmt not in B.MOE_MX:
+        raise ValueError(f"unknown format {fmt!r}")
+    if values is not None and (values.dtype != x.dtype or values.shape != (rows, cols) or values.device != x.device):
+        raise ValueError(f"values: {x.dtype} {(rows, cols)} on {x.device} is needed")
+    f = B.MOE_MX[fmt]
+    if out is None:
+        codes = torch.empty(rows, cols // 2, dtype=torch.uint8, device=x.device)
+        scales = torch.empty(B.moe_mx_scales_bytes(f, rows, cols), dtype=torch.uint8, device=x.device)
+        out = MxTensor(fmt, codes, scales, rows, cols, scale_exp=scale_exp)
+    elif (out.format, out.rows, out.cols, out.groups, out.scale_exp) != (fmt, rows, cols, 1, scale_exp) or \
+            out.codes.device != x.device:
+        raise ValueError("out has another format, size, exponent or device")
+    _call(x, B.moe_mx_quantize, f, _ptr(x), _DTYPE[x.dtype], ld, x.shape[0], cols, _ptr(row_index), rows, scale_exp,
+          _ptr(out.codes), _ptr(out.scales), _ptr(values), 0 if values is None else _rows("values", values))
+    return out
+
+
+def mx_dequantize(q: MxTensor, dtype: torch.dtype = torch.float32) -> torch.Tensor:
+    """The values of q, [rows][cols] (one group)."""
+    if dtype not in _DTYPE:
+        raise ValueError(f"bf16 or fp32, got {dtype}")
+    if q.groups != 1:
+        raise ValueError("one group at a time")
+    out = torch.empty(q.rows, q.cols, dtype=dtype, device=q.codes.device)
+    _call(out, B.moe_mx_dequantize, B.MOE_MX[q.format], _ptr(q.codes), _ptr(q.scales), q.rows, q.cols, q.scale_exp,
+          _ptr(out), _DTYPE[dtype], q.cols)
+    return out
+
+
+def mx_gemm(a: MxTensor, w: MxTensor, group_start: Optional[torch.Tensor] = None,
+            group_rows: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+            alpha: Optional[torch.Tensor] = None, activation: Optional[str] = None, out: Optional[torch.Tensor] = None,
+            dtype: torch.dtype = torch.bfloat16, status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """act(alpha_g a w_g^T + bias_g) for the rows of every group g: rows group_start[g] ..
+    + group_rows[g] of a (int32, starts multiples of 128), or all rows with one group and
+    neither given. Rows of no group are left as they were in `out`, or hold anything where
+    `out` is not given. status: an int32 tensor of one zero, whose bit 0 reports a wait that
+    gave up and bit 1 a segment outside the rows."""
+    if a.format != w.format or a.cols != w.cols:
+        raise ValueError(f"operands differ: {a.format} of {a.cols} columns, {w.format} of {w.cols}")
+    if a.groups != 1:
+        raise ValueError("a has one group of rows")
+    like = a.codes
+    if w.codes.device != like.device:
+        raise ValueError("operands on different devices")
+    G, n = w.groups, w.rows
+    for name, t in (("group_start", group_start), ("group_rows", group_rows)):
+        if t is not None:
+            _array(name, t, like, torch.int32)
+            if t.numel() < G:
+                raise ValueError(f"{name}: one entry for each of {G} groups is needed")
+    _array("bias", bias, like, torch.float32, (G, n))
+    _array("alpha", alpha, like, torch.float32, (G,))
+    _array("status", status, like, torch.int32, (1,))
+    if out is None:
+        out = torch.empty(a.rows, n, dtype=dtype, device=like.device)
+    elif out.device != like.device or out.shape[0] != a.rows:
+        raise ValueError(f"out: {a.rows} rows on {like.device} are needed")
+    ld = _rows("out", out, n)
+    act = B.MOE_ACT_NONE if activation in (None, "none") else B.MOE_ACT[activation]
+    args = B.MoeMxGemm(B.MOE_MX[a.format], a.rows, n, a.cols, G, a.scale_exp + w.scale_exp, act, _DTYPE[out.dtype], ld,
+                       _ptr(a.codes), _ptr(a.scales), _ptr(w.codes), _ptr(w.scales), _ptr(group_start),
+                       _ptr(group_rows), _ptr(bias), _ptr(alpha), _ptr(out), _ptr(status))
+    _call(like, B.moe_mx_gemm, args)
+    return out

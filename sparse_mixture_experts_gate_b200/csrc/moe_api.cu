@@ -114,6 +114,20 @@ bool encode_u8_2d(CUtensorMap *m, const void *base, uint64_t inner, uint64_t row
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+// 512-byte scale tiles [blocks][tiles] read in boxes of box_tiles tiles (as
+// 64-bit words; no swizzle, tiles past a block's end read as zeros).
+bool encode_scale_tiles(CUtensorMap *m, const void *base, uint64_t tiles, uint64_t blocks, uint32_t box_tiles) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn || blocks == 0) return false;
+    cuuint64_t dims[2] = {tiles * 64, blocks};
+    cuuint64_t strides[1] = {tiles * 512};
+    cuuint32_t box[2] = {box_tiles * 64, 1};
+    cuuint32_t es[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, const_cast<void *>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 }  // namespace moe
 
 struct moe_layer {

@@ -307,4 +307,7 @@ int report_error(int code, const char *msg);
 // of 128 bytes x box_rows, 128B swizzle.
 bool encode_u8_2d(CUtensorMap *m, const void *base, uint64_t inner, uint64_t rows, uint32_t box_rows);
 
+// Tensor map of 512-byte scale tiles [blocks][tiles], boxes of box_tiles tiles.
+bool encode_scale_tiles(CUtensorMap *m, const void *base, uint64_t tiles, uint64_t blocks, uint32_t box_tiles);
+
 }  // namespace moe

@@ -53,7 +53,6 @@ struct MxDequantArgs {
 cudaError_t launch_mx_dequantize(const MxDequantArgs &a, int format, bool bf16, cudaStream_t s);
 
 struct MxGemmArgs {
-    const uint8_t *a_scales, *w_scales;
     const int32_t *group_start, *group_rows;  // [G] or null (one group of all rows)
     int rows, N, K, G;
     const float *bias;   // [G][N] or null
@@ -63,11 +62,15 @@ struct MxGemmArgs {
     void *out;
     int out_f32;
     int64_t out_ld;
-    int wide_ok;         // out and out_ld allow 4-byte stores of bf16 pairs
+    int vec_ok;          // bf16 outputs: out and out_ld allow 16-byte stores
     uint32_t *status;    // or null
 };
-cudaError_t launch_mx_gemm(const CUtensorMap &map_w, const CUtensorMap &map_a, const MxGemmArgs &a, int format,
-                           int num_sms, cudaStream_t s);
+// Tensor maps of the codes (boxes of 128 bytes x 128 weight rows or 16 token
+// rows) and of the scale tiles (boxes of one stage's tiles of one row block).
+struct MxMaps {
+    CUtensorMap w, a, sw, sa;
+};
+cudaError_t launch_mx_gemm(const MxMaps &m, const MxGemmArgs &a, int format, int num_sms, cudaStream_t s);
 
 // Device status bits the product adds to kDevTimeout.
 enum : uint32_t { kDevBadGroup = 2u };
@@ -121,15 +124,6 @@ __device__ __forceinline__ void tc_mma_mx(uint32_t d_tmem, uint64_t a_desc, uint
     if constexpr (FMT == kNvFp4 && CG == 1) MOE_MX_MMA("mxf4nvf4", "1", "4X");
     if constexpr (FMT == kNvFp4 && CG == 2) MOE_MX_MMA("mxf4nvf4", "2", "4X");
 #undef MOE_MX_MMA
-}
-
-// Untiled bulk copy into shared memory (16-byte aligned addresses and size),
-// completing on `bar`.
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
 }
 
 // The value of an E4M3 byte (0x7f and 0xff are NaN).

@@ -301,13 +301,15 @@ int moe_mx_gemm(const moe_mx_gemm_t *p, void *stream_v) {
     if (p->rows == 0) return MOE_OK;
     int sms = 0;
     if ((rc = device_sms(&sms)) != MOE_OK) return rc;
-    CUtensorMap mw, ma;
-    if (!encode_u8_2d(&mw, p->w_codes, p->k / 2, (uint64_t)p->groups * p->n, 128) ||
-        !encode_u8_2d(&ma, p->a_codes, p->k / 2, p->rows, 16))
-        return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the codes");
+    MxMaps m;
+    const uint64_t tiles = mx_scale_tiles(p->k, block_of(p->format));
+    if (!encode_u8_2d(&m.w, p->w_codes, p->k / 2, (uint64_t)p->groups * p->n, 128) ||
+        !encode_u8_2d(&m.a, p->a_codes, p->k / 2, p->rows, 16) ||
+        !encode_scale_tiles(&m.sw, p->w_scales, tiles, (uint64_t)p->groups * ((p->n + 127) / 128),
+                            256 / (4 * block_of(p->format))) ||
+        !encode_scale_tiles(&m.sa, p->a_scales, tiles, ((uint64_t)p->rows + 127) / 128, 256 / (4 * block_of(p->format))))
+        return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the codes or scales");
     MxGemmArgs a;
-    a.a_scales = static_cast<const uint8_t *>(p->a_scales);
-    a.w_scales = static_cast<const uint8_t *>(p->w_scales);
     a.group_start = p->group_start;
     a.group_rows = p->group_rows;
     a.rows = p->rows;
@@ -321,9 +323,9 @@ int moe_mx_gemm(const moe_mx_gemm_t *p, void *stream_v) {
     a.out = p->out;
     a.out_f32 = p->out_dtype == MOE_DTYPE_FP32;
     a.out_ld = p->out_ld;
-    a.wide_ok = !a.out_f32 && aligned(p->out, 4) && p->out_ld % 2 == 0;
+    a.vec_ok = !a.out_f32 && aligned(p->out, 16) && p->out_ld % 8 == 0;
     a.status = p->status;
-    return launched(launch_mx_gemm(mw, ma, a, p->format, sms, as_stream(stream_v)), "moe_mx_gemm");
+    return launched(launch_mx_gemm(m, a, p->format, sms, as_stream(stream_v)), "moe_mx_gemm");
 }
 
 }  // extern "C"

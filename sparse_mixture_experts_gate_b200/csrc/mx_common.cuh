@@ -41,7 +41,7 @@ struct MxQuantArgs {
     int64_t values_ld;
     float post;                // 2^scale_exp
 };
-cudaError_t launch_mx_quantize(const MxQuantArgs &a, int format, bool bf16, cudaStream_t s);
+cudaError_t launch_mx_quantize(const MxQuantArgs &a, int format, bool bf16, int num_sms, cudaStream_t s);
 
 struct MxDequantArgs {
     const uint8_t *codes, *scales;
@@ -65,10 +65,10 @@ struct MxGemmArgs {
     int vec_ok;          // bf16 outputs: out and out_ld allow 16-byte stores
     uint32_t *status;    // or null
 };
-// Tensor maps of the codes (boxes of 128 bytes x 128 weight rows or 16 token
+// Tensor maps of the codes (boxes of 128 bytes x 128 weight rows, 16 or 96 token
 // rows) and of the scale tiles (boxes of one stage's tiles of one row block).
 struct MxMaps {
-    CUtensorMap w, a, sw, sa;
+    CUtensorMap w, a, a96, sw, sa;
 };
 cudaError_t launch_mx_gemm(const MxMaps &m, const MxGemmArgs &a, int format, int num_sms, cudaStream_t s);
 

@@ -7,34 +7,40 @@
 // fp32 and rounded once, to the output's type.
 //
 // Operand roles. The MMA's M side is the output features (rows of W[g]) and its
-// N side a token tile of up to TILE rows of one group, so a group of a few rows
-// costs an MMA of a few columns. Unit = (token tile, feature tile); every CTA
-// builds the groups' tile prefix in shared memory and takes its share of the
-// units in steps of the grid.
+// N side a token tile of one group, so a group of a few rows costs an MMA of a few
+// columns. Unit = (token tile, feature tile); every CTA builds the groups' tile
+// prefix in shared memory and takes its share of the units in steps of the grid.
 //
-// Two forms. Long segments run on CTA pairs (cta_group::2): 256 features x 192
-// tokens, each CTA staging its 128 weight rows and half of the tokens, because
-// the operands' way from L2 is what bounds them. Short segments (a few tokens for
-// each expert: the weights' bytes bound them) run on single CTAs with 128
-// features x up to 64 tokens and a deeper pipeline.
+// Two forms. Long segments are bound by the operands' way from L2 (about 10 TB/s
+// here), so they run on CTA pairs (cta_group::2) whose unit is 256 features x 384
+// tokens, as two MMAs of 192 tokens into one accumulator each: each CTA stages its
+// 128 weight rows and half of the tokens. Short segments (a few tokens for each
+// expert) are bound by the weights' bytes: single CTAs, 128 features x up to 64
+// tokens, a deeper pipeline, two accumulators in turn.
 //
 // Per CTA (320 threads): warp 0 loads codes (TMA, 128B swizzle, 256 elements
 // of K a stage) and scale tiles, signalling the (leader's) stage barrier; warp
 // 1 owns TMEM and, in the leader, copies a stage's scale tiles into TMEM
 // (tcgen05.cp, both CTAs') and issues its MMAs; warps 2..9 drain this CTA's 128
-// features of the accumulator, two warps for each quarter of the TMEM lanes.
+// features of the accumulators, two warps for each quarter of the TMEM lanes. The
+// loading and issuing warps run their loops with all lanes and elect one only for
+// the instructions themselves: descriptors then stay in uniform registers (with
+// one lane in the loop, issuing took longer than the products: 121 us instead of
+// 91 for 128 experts of 1536 x 4096 with a row or a few each).
 //
-// TMEM (512 columns): two accumulators of TILE columns and, in the rest, as many
-// buffers of scale columns as there are stages, or fit: then a buffer is
-// filled again only once the MMAs that read it have completed (their stage's
-// commit), so no copy passes an MMA. A token tile starts at a multiple of 64 rows
-// of the 128-row scale tiles, so its first scale column is 0 or 2.
+// TMEM (512 columns): two accumulators and, in the rest, as many buffers of scale
+// columns as there are stages, or fit: a buffer is filled again only once the MMAs
+// that read it have completed (their stage's commit), so no copy passes an MMA. A
+// token tile starts at a multiple of 64 rows of the 128-row scale tiles, so its
+// first scale column is even.
 //
 // Epilogue of bf16 outputs: TMEM is read in 16 x 256-bit pieces, whose register
 // layout (a lane holds two neighbouring tokens of one feature) is the one that
 // stmatrix.trans takes, so a warp turns 32 tokens x 32 features around through a
 // shared buffer of its own without shuffles, and stores each token's 64 bytes
-// with 16-byte stores. fp32 outputs are stored from lane = feature directly.
+// with 16-byte stores. A warp takes all of its part of an accumulator into
+// registers and hands the accumulator back before it computes. fp32 outputs are
+// stored from lane = feature directly.
 //
 // Every wait is bounded; a role that gives up sets the block's status word, the
 // others stop, and the block ends after its copies and MMAs have drained.
@@ -56,13 +62,16 @@ constexpr int kPitch = 80;                // bytes of a staged token row (64 use
 constexpr int kStageOut = 32 * kPitch;    // one warp's output buffer
 constexpr int kActRuntime = -2;           // fp32 outputs: the activation is looked up at run time
 
-template <int FMT, int TILE, int CG>
+// TILE tokens per accumulator, SUB accumulators per unit.
+template <int FMT, int TILE, int SUB, int CG>
 struct Cfg {
+    static constexpr int kUnitTok = TILE * SUB;
     static constexpr int kSfTiles = kStageK / MxFormat<FMT>::kTileK;  // scale tiles along K per stage
-    static constexpr int kRowBlocks = TILE > 64 ? 2 : 1;              // 128-row scale tiles under a token tile
+    static constexpr int kRowBlocks = (kUnitTok + 127) / 128;         // 128-row scale tiles under a unit's tokens
     static constexpr int kSfA = kSfTiles * 512;                       // weight scales
     static constexpr int kSfB = kRowBlocks * kSfTiles * 512;          // token scales
-    static constexpr int kB = TILE / CG * 128;
+    static constexpr int kSub = TILE / CG * 128;                      // token codes of one accumulator
+    static constexpr int kB = SUB * kSub;
     static constexpr int kStage = kWBytes + kB + kSfA + kSfB;
     static constexpr int kFixed = 1024 + kEpiWarps * kStageOut + 512 + (kMaxGroups + 1) * 4 + 128;
     static constexpr int kFit = (232448 - kFixed) / kStage;
@@ -75,12 +84,20 @@ struct Cfg {
     static constexpr int kSfBufs = kSfFit < kStages ? kSfFit : kStages;
     static constexpr int kStep = 16 * CG;                             // token rows: a TMA box per CTA
     static_assert(kStages >= 4 && kSfBufs >= 2, "pipeline depth");
-    static_assert(kB % 1024 == 0, "operand tiles keep the 1024-byte swizzle alignment");
+    static_assert(SUB == 1 || kUnitTok % 128 == 0, "units start on a scale tile");
+    static_assert(kSub % 1024 == 0, "operand tiles keep the 1024-byte swizzle alignment");
 };
 
 struct Unit {
     int g, row0, ntok, feat0;
 };
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0u;
+}
 
 __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -99,10 +116,10 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
                  : "memory");
 }
 
-template <int FMT, int TILE, int CG, int ACT>
+template <int FMT, int TILE, int SUB, int CG, int ACT>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_gemm_kernel(const __grid_constant__ MxMaps m, const MxGemmArgs a) {
-    using C = Cfg<FMT, TILE, CG>;
+    using C = Cfg<FMT, TILE, SUB, CG>;
     constexpr int kStages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -122,6 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&m.w);
         tma_prefetch_desc(&m.a);
+        if (CG == 2) tma_prefetch_desc(&m.a96);
         tma_prefetch_desc(&m.sw);
         tma_prefetch_desc(&m.sa);
         for (int i = 0; i < kStages; ++i) {
@@ -157,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // A segment that is not where the layout allows it is not computed.
             const bool fits = rows >= 0 && start >= 0 && start % 128 == 0 && start <= a.rows && rows <= a.rows - start;
             if (!fits && rows != 0) atomicOr(status, kDevBadGroup);
-            v = fits ? (rows + TILE - 1) / TILE : 0;
+            v = fits ? (rows + C::kUnitTok - 1) / C::kUnitTok : 0;
         }
         int s = v;
 #pragma unroll
@@ -201,8 +219,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int start = a.group_start ? a.group_start[lo] : 0;
         const int rows = a.group_rows ? a.group_rows[lo] : a.rows;
-        const int off = (tt - prefix[lo]) * TILE;
-        return Unit{lo, start + off, min(TILE, rows - off), (u - tt * n_ft) * kFeat * CG};
+        const int off = (tt - prefix[lo]) * C::kUnitTok;
+        return Unit{lo, start + off, min(C::kUnitTok, rows - off), (u - tt * n_ft) * kFeat * CG};
     };
     auto commit_all = [&](uint64_t *bar) {
         if constexpr (CG == 2) tc_commit_pair_mc(bar, 0x3);
@@ -212,127 +230,185 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
+        const bool one = elect_one();
         const int NB = (a.N + 127) / 128;
         uint32_t it = 0;
         for (int u = first; u < total && ok; u += step) {
             const Unit w = unit_of(u);
-            const int boxes = (w.ntok + C::kStep - 1) / C::kStep;  // 16-row boxes of this CTA
             const int nrb = (w.row0 % 128 + w.ntok + 127) / 128;
             const int feat = w.feat0 + static_cast<int>(rank) * kFeat;
-            const int wrow = w.g * a.N + feat, trow = w.row0 + static_cast<int>(rank) * boxes * 16;
+            const int wrow = w.g * a.N + feat;
             // The second CTA of a last feature tile may have no weight scales: it reads the group's last ones.
             const int wblk = w.g * NB + min(feat / 128, NB - 1), tblk = w.row0 / 128;
-            const uint32_t bytes = CG * (kWBytes + boxes * 2048 + C::kSfA + nrb * C::kSfTiles * 512);
+            int boxes[SUB], rows = 0;  // 16-row boxes of this CTA's part of each accumulator's tokens
+#pragma unroll
+            for (int s = 0; s < SUB; ++s) {
+                boxes[s] = (min(TILE, max(w.ntok - s * TILE, 0)) + C::kStep - 1) / C::kStep;
+                rows += boxes[s] * 16;
+            }
+            const uint32_t bytes = CG * (kWBytes + rows * 128 + C::kSfA + nrb * C::kSfTiles * 512);
             for (int kb = 0; kb < kblocks; ++kb, ++it) {
                 const int st = it % kStages;
-                const uint32_t ph = (it / kStages) & 1u;
-                int got = 1;
-                if (lane == 0) got = mbar_wait(&empty[st], ph ^ 1u, status) ? 1 : 0;
-                if (!__shfl_sync(0xffffffffu, got, 0)) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], ((it / kStages) & 1u) ^ 1u, status))) {
                     ok = false;
                     break;
                 }
-                if (lane == 0 && leader) mbar_arrive_expect_tx(&full[st], bytes);
+                if (one) {
+                    const uint32_t bar = CG == 2 ? mapa_shared(smem_u32(&full[st]), 0) : 0u;
+                    auto load = [&](const CUtensorMap *map, void *dst, int x, int y) {
+                        if constexpr (CG == 2) tma_load_2d_pair(map, bar, dst, x, y);
+                        else tma_load_2d(map, &full[st], dst, x, y);
+                    };
+                    if (leader) mbar_arrive_expect_tx(&full[st], bytes);
+                    load(&m.w, sW + st * kWBytes, kb * 128, wrow);
+                    load(&m.sw, sSfW + st * C::kSfA, kb * C::kSfTiles * 64, wblk);
+#pragma unroll
+                    for (int s = 0; s < SUB; ++s) {
+                        uint8_t *dst = sT + st * C::kB + s * C::kSub;
+                        const int row = w.row0 + s * TILE + static_cast<int>(rank) * boxes[s] * 16;
+                        if (CG == 2 && boxes[s] == TILE / C::kStep) {
+                            load(&m.a96, dst, kb * 128, row);
+                        } else {
+                            for (int b = 0; b < boxes[s]; ++b) load(&m.a, dst + b * 2048, kb * 128, row + b * 16);
+                        }
+                    }
+                    for (int b = 0; b < nrb; ++b)
+                        load(&m.sa, sSfT + st * C::kSfB + b * C::kSfTiles * 512, kb * C::kSfTiles * 64, tblk + b);
+                }
                 __syncwarp();
-                auto load = [&](const CUtensorMap *map, void *dst, int x, int y) {
-                    if constexpr (CG == 2) tma_load_2d_pair(map, mapa_shared(smem_u32(&full[st]), 0), dst, x, y);
-                    else tma_load_2d(map, &full[st], dst, x, y);
-                };
-                if (lane == 0) load(&m.w, sW + st * kWBytes, kb * 128, wrow);
-                if (lane < boxes) load(&m.a, sT + st * C::kB + lane * 2048, kb * 128, trow + lane * 16);
-                if (lane == 16) load(&m.sw, sSfW + st * C::kSfA, kb * C::kSfTiles * 64, wblk);
-                if (lane >= 17 && lane - 17 < nrb)
-                    load(&m.sa, sSfT + st * C::kSfB + (lane - 17) * C::kSfTiles * 512, kb * C::kSfTiles * 64,
-                         tblk + lane - 17);
             }
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA (leader)
-        if (leader && lane == 0) {
-            uint32_t it = 0, tcount = 0;
+        if (leader) {
+            const bool one = elect_one();
+            uint32_t it = 0, uses[SUB] = {}, tcount = 0;
             for (int u = first; u < total && ok; u += step, ++tcount) {
                 const Unit w = unit_of(u);
                 const int nrb = (w.row0 % 128 + w.ntok + 127) / 128;
-                const uint32_t idesc = mx_idesc<FMT>(kFeat * CG, (w.ntok + C::kStep - 1) / C::kStep * C::kStep);
-                const uint32_t shift = (w.row0 % 128) / 32;  // first scale column of the tile
-                const uint32_t acc = tcount & 1u, use = tcount >> 1;
-                if (!mbar_wait(&tempty[acc], (use & 1u) ^ 1u, status)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after_sync();
-                const uint32_t d = tmem_base + acc * TILE;
-                for (int kb = 0; kb < kblocks; ++kb, ++it) {
+                const uint32_t shift = (w.row0 % 128) / 32;  // first scale column of the unit's tokens
+                int cols[SUB];
+#pragma unroll
+                for (int s = 0; s < SUB; ++s)
+                    cols[s] = (min(TILE, max(w.ntok - s * TILE, 0)) + C::kStep - 1) / C::kStep * C::kStep;
+                for (int kb = 0; kb < kblocks && ok; ++kb, ++it) {
                     const int st = it % kStages;
                     // The MMAs that read this scale buffer before are done.
-                    if (C::kSfBufs < kStages && it >= C::kSfBufs &&
-                        !mbar_wait(&empty[(it - C::kSfBufs) % kStages], ((it - C::kSfBufs) / kStages) & 1u, status)) {
-                        ok = false;
-                        break;
-                    }
-                    if (!mbar_wait(&full[st], (it / kStages) & 1u, status)) {
+                    if (C::kSfBufs < kStages && it >= C::kSfBufs)
+                        ok = mbar_wait(&empty[(it - C::kSfBufs) % kStages], ((it - C::kSfBufs) / kStages) & 1u, status);
+                    if (ok) ok = mbar_wait(&full[st], (it / kStages) & 1u, status);
+                    if (!__all_sync(0xffffffffu, ok)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after_sync();
                     const uint32_t sfa = tmem_base + C::kScaleCol + (it % C::kSfBufs) * C::kSfCols;
                     const uint32_t sfb = sfa + C::kSfColsA;
-                    const uint64_t ad = sw128_kmajor_desc(smem_u32(sW + st * kWBytes));
-                    const uint64_t bd = sw128_kmajor_desc(smem_u32(sT + st * C::kB));
-                    const uint64_t da = scale_tile_desc(smem_u32(sSfW + st * C::kSfA));
-                    const uint64_t db = scale_tile_desc(smem_u32(sSfT + st * C::kSfB));
+                    if (one) {
+                        const uint64_t da = scale_tile_desc(smem_u32(sSfW + st * C::kSfA));
+                        const uint64_t db = scale_tile_desc(smem_u32(sSfT + st * C::kSfB));
+#pragma unroll
+                        for (int j = 0; j < C::kSfTiles; ++j) {
+                            tc_cp_scales<CG>(sfa + 4 * j, da + 32u * j);
+#pragma unroll
+                            for (int b = 0; b < C::kRowBlocks; ++b)
+                                if (b < nrb)
+                                    tc_cp_scales<CG>(sfb + (j * C::kRowBlocks + b) * 4, db + 32u * (b * C::kSfTiles + j));
+                        }
+                    }
                     const int steps = (min(kStageK, a.K - kb * kStageK) + 63) / 64;
 #pragma unroll
-                    for (int j = 0; j < C::kSfTiles; ++j) {
-                        tc_cp_scales<CG>(sfa + 4 * j, da + 32u * j);
-                        tc_cp_scales<CG>(sfb + j * C::kRowBlocks * 4, db + 32u * j);
-                        if (nrb > 1)
-                            tc_cp_scales<CG>(sfb + j * C::kRowBlocks * 4 + 4, db + 32u * (C::kSfTiles + j));
-                    }
+                    for (int s = 0; s < SUB; ++s) {
+                        if (cols[s] == 0) continue;
+                        const uint32_t acc = SUB == 2 ? s : tcount & 1u;
+                        if (kb == 0) {  // the accumulator has been drained
+                            const uint32_t use = SUB == 2 ? uses[s] : tcount >> 1;
+                            if (!__all_sync(0xffffffffu, mbar_wait(&tempty[acc], (use & 1u) ^ 1u, status))) {
+                                ok = false;
+                                break;
+                            }
+                            ++uses[s];
+                            tc_fence_after_sync();
+                        }
+                        if (one) {
+                            const uint32_t idesc = mx_idesc<FMT>(kFeat * CG, cols[s]);
+                            const uint64_t ad = sw128_kmajor_desc(smem_u32(sW + st * kWBytes));
+                            const uint64_t bd = sw128_kmajor_desc(smem_u32(sT + st * C::kB + s * C::kSub));
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        if (kk >= steps) break;
-                        // 64 elements: half of an MXFP4 scale tile's 4 scales, a whole NVFP4 one's.
-                        const int j = FMT == kMxFp4 ? kk / 2 : kk;
-                        const uint32_t id = FMT == kMxFp4 ? 2u * (kk & 1) : 0u;
-                        tc_mma_mx<FMT, CG>(d, ad + 2u * kk, bd + 2u * kk, idesc | mx_idesc_sf(id), sfa + 4 * j,
-                                           sfb + j * C::kRowBlocks * 4 + shift, (kb | kk) != 0 ? 1u : 0u);
+                            for (int kk = 0; kk < 4; ++kk) {
+                                if (kk >= steps) break;
+                                // 64 elements: half of an MXFP4 scale tile's 4 scales, a whole NVFP4 one's.
+                                const int j = FMT == kMxFp4 ? kk / 2 : kk;
+                                const uint32_t id = FMT == kMxFp4 ? 2u * (kk & 1) : 0u;
+                                tc_mma_mx<FMT, CG>(tmem_base + acc * TILE, ad + 2u * kk, bd + 2u * kk,
+                                                   idesc | mx_idesc_sf(id), sfa + 4 * j,
+                                                   sfb + j * C::kRowBlocks * 4 + shift + s * (TILE / 32),
+                                                   (kb | kk) != 0 ? 1u : 0u);
+                            }
+                            if (kb == kblocks - 1) commit_all(&tfull[acc]);
+                        }
                     }
-                    commit_all(&empty[st]);
+                    if (ok && one) commit_all(&empty[st]);
+                    __syncwarp();
                 }
-                if (ok) commit_all(&tfull[acc]);
             }
-            if constexpr (CG == 2) tc_commit_pair(mma_done);
-            else tc_commit(mma_done);
+            if (one) {
+                if constexpr (CG == 2) tc_commit_pair(mma_done);
+                else tc_commit(mma_done);
+            }
+            __syncwarp();
             mbar_wait_drain(mma_done, 0u);
         }
-        __syncwarp();
     } else {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;             // the TMEM lane quarter this warp may read
         const int half = (warp - 2) >> 2;   // which of the quarter's two warps: every other 32 tokens
-        const uint32_t buf = smem_u32(sOut + (warp - 2) * kStageOut);
-        uint32_t tcount = 0;
-        for (int u = first; u < total; u += step, ++tcount) {
+        const uint8_t *own = sOut + (warp - 2) * kStageOut;
+        const uint32_t buf = smem_u32(own);
+        auto release = [&](uint32_t acc) {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (CG == 2) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
+                else mbar_arrive(&tempty[acc]);
+            }
+        };
+        uint32_t uses[SUB] = {}, tcount = 0;
+        for (int u = first; u < total && ok; u += step, ++tcount) {
             const Unit w = unit_of(u);
-            const uint32_t acc = tcount & 1u, use = tcount >> 1;
             const int f0 = w.feat0 + static_cast<int>(rank) * kFeat + q * 32;
             const float mul = a.post * (a.alpha ? __ldg(a.alpha + w.g) : 1.f);
             auto bias_of = [&](int f) { return a.bias && f < a.N ? __ldg(a.bias + (int64_t)w.g * a.N + f) : 0.f; };
-            int got = 1;
-            if constexpr (ACT != kActRuntime) {
-                float bv[4];
+            float bv[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) bv[i] = bias_of(f0 + lane / 4 + 8 * i);
+            for (int i = 0; i < 4; ++i) bv[i] = bias_of(ACT == kActRuntime ? f0 + lane : f0 + lane / 4 + 8 * i);
+#pragma unroll
+            for (int s = 0; s < SUB; ++s) {
+                const int ntok = min(TILE, w.ntok - s * TILE), row0 = w.row0 + s * TILE;
+                if (ntok <= 0) break;
+                const uint32_t acc = SUB == 2 ? s : tcount & 1u;
+                const uint32_t use = SUB == 2 ? uses[s] : tcount >> 1;
+                int got = 1;
                 if (lane == 0) got = mbar_wait_idle(&tfull[acc], use & 1u, status) ? 1 : 0;
-                if (!__shfl_sync(0xffffffffu, got, 0)) break;
+                ++uses[s];
+                if (!__shfl_sync(0xffffffffu, got, 0)) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_after_sync();
                 const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * TILE;
-                for (int c = half * 32; c < w.ntok; c += 64) {
-                    uint32_t lo[16], hi[16];  // features 0..15 and 16..31 of the quarter
-                    tmem_ld_16x256b_x4(taddr + c, lo);
-                    tmem_ld_16x256b_x4(taddr + (16u << 16) + c, hi);
+                if constexpr (ACT != kActRuntime) {
+                    constexpr int kChunks = TILE / 64;
+                    uint32_t lo[kChunks][16], hi[kChunks][16];  // features 0..15 and 16..31 of the quarter
+#pragma unroll
+                    for (int i = 0; i < kChunks; ++i) {
+                        if (half * 32 + 64 * i < ntok) {
+                            tmem_ld_16x256b_x4(taddr + half * 32 + 64 * i, lo[i]);
+                            tmem_ld_16x256b_x4(taddr + (16u << 16) + half * 32 + 64 * i, hi[i]);
+                        }
+                    }
                     tmem_ld_wait();
+                    release(acc);
                     auto pack = [&](uint32_t x, uint32_t y, float b) {
                         const __nv_bfloat162 p =
                             __floats2bfloat162_rn(activate_t<ACT>(fmaf(__uint_as_float(x), mul, b)),
@@ -340,56 +416,53 @@ __global__ void __launch_bounds__(kThreads, 1)
                         return *reinterpret_cast<const uint32_t *>(&p);
                     };
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        stmatrix_x4_trans(buf + (8 * j + lane % 8) * kPitch + lane / 8 * 16,
-                                          pack(lo[4 * j], lo[4 * j + 1], bv[0]), pack(lo[4 * j + 2], lo[4 * j + 3], bv[1]),
-                                          pack(hi[4 * j], hi[4 * j + 1], bv[2]),
-                                          pack(hi[4 * j + 2], hi[4 * j + 3], bv[3]));
-                    __syncwarp();
-                    const int f = f0 + lane % 4 * 8;
-                    const uint8_t *src = sOut + (warp - 2) * kStageOut + lane % 4 * 16;
+                    for (int i = 0; i < kChunks; ++i) {
+                        const int c = half * 32 + 64 * i;
+                        if (c >= ntok) break;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int t = c + 8 * i + lane / 4;
-                        const uint4 v = *reinterpret_cast<const uint4 *>(src + (8 * i + lane / 4) * kPitch);
-                        if (t < w.ntok && f < a.N) {
-                            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.out) + (int64_t)(w.row0 + t) * a.out_ld + f;
-                            if (a.vec_ok && f + 8 <= a.N) {
-                                *reinterpret_cast<uint4 *>(o) = v;
-                            } else {
-                                const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+                        for (int j = 0; j < 4; ++j)
+                            stmatrix_x4_trans(buf + (8 * j + lane % 8) * kPitch + lane / 8 * 16,
+                                              pack(lo[i][4 * j], lo[i][4 * j + 1], bv[0]),
+                                              pack(lo[i][4 * j + 2], lo[i][4 * j + 3], bv[1]),
+                                              pack(hi[i][4 * j], hi[i][4 * j + 1], bv[2]),
+                                              pack(hi[i][4 * j + 2], hi[i][4 * j + 3], bv[3]));
+                        __syncwarp();
+                        const int f = f0 + lane % 4 * 8;
 #pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    if (f + k < a.N)
-                                        o[k] = __ushort_as_bfloat16(static_cast<unsigned short>(words[k / 2] >> (16 * (k & 1))));
+                        for (int k = 0; k < 4; ++k) {
+                            const int t = c + 8 * k + lane / 4;
+                            const uint4 v =
+                                *reinterpret_cast<const uint4 *>(own + (8 * k + lane / 4) * kPitch + lane % 4 * 16);
+                            if (t < ntok && f < a.N) {
+                                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.out) + (int64_t)(row0 + t) * a.out_ld + f;
+                                if (a.vec_ok && f + 8 <= a.N) {
+                                    *reinterpret_cast<uint4 *>(o) = v;
+                                } else {
+                                    const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e)
+                                        if (f + e < a.N)
+                                            o[e] = __ushort_as_bfloat16(
+                                                static_cast<unsigned short>(words[e / 2] >> (16 * (e & 1))));
+                                }
                             }
                         }
+                        __syncwarp();
                     }
-                    __syncwarp();
-                }
-            } else {
-                const int f = f0 + lane;
-                const float bv = bias_of(f);
-                if (lane == 0) got = mbar_wait_idle(&tfull[acc], use & 1u, status) ? 1 : 0;
-                if (!__shfl_sync(0xffffffffu, got, 0)) break;
-                tc_fence_after_sync();
-                const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * TILE;
-                for (int c = half * 16; c < w.ntok; c += 32) {
-                    uint32_t r[16];
-                    tmem_ld_32x32b_x16(taddr + c, r);
-                    tmem_ld_wait();
-                    float *o = static_cast<float *>(a.out) + (int64_t)(w.row0 + c) * a.out_ld + f;
+                } else {
+                    const int f = f0 + lane;
+                    for (int c = half * 16; c < ntok; c += 32) {
+                        uint32_t r[16];
+                        tmem_ld_32x32b_x16(taddr + c, r);
+                        tmem_ld_wait();
+                        float *o = static_cast<float *>(a.out) + (int64_t)(row0 + c) * a.out_ld + f;
 #pragma unroll
-                    for (int t = 0; t < 16; ++t)
-                        if (f < a.N && c + t < w.ntok)
-                            o[t * a.out_ld] = activate(a.act, fmaf(__uint_as_float(r[t]), mul, bv));
+                        for (int t = 0; t < 16; ++t)
+                            if (f < a.N && c + t < ntok)
+                                o[t * a.out_ld] = activate(a.act, fmaf(__uint_as_float(r[t]), mul, bv[0]));
+                    }
+                    release(acc);
                 }
-            }
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-                if constexpr (CG == 2) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
-                else mbar_arrive(&tempty[acc]);
             }
         }
     }
@@ -410,12 +483,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int FMT, int TILE, int CG, int ACT>
+template <int FMT, int TILE, int SUB, int CG, int ACT>
 cudaError_t launch(const MxMaps &m, const MxGemmArgs &a, int num_sms, cudaStream_t s) {
-    using C = Cfg<FMT, TILE, CG>;
-    cudaError_t e = set_smem_limit_once<mx_gemm_kernel<FMT, TILE, CG, ACT>>(C::kSmem);
+    using C = Cfg<FMT, TILE, SUB, CG>;
+    cudaError_t e = set_smem_limit_once<mx_gemm_kernel<FMT, TILE, SUB, CG, ACT>>(C::kSmem);
     if (e != cudaSuccess) return e;
-    const int64_t most = ((int64_t)a.rows / TILE + a.G) * ((a.N + kFeat * CG - 1) / (kFeat * CG));
+    const int64_t most = ((int64_t)a.rows / C::kUnitTok + a.G) * ((a.N + kFeat * CG - 1) / (kFeat * CG));
     if (most > INT32_MAX) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(CG * static_cast<unsigned>(std::min<int64_t>(most, num_sms / CG)), 1, 1);
@@ -429,17 +502,17 @@ cudaError_t launch(const MxMaps &m, const MxGemmArgs &a, int num_sms, cudaStream
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CG == 2 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, mx_gemm_kernel<FMT, TILE, CG, ACT>, m, a);
+    return cudaLaunchKernelEx(&cfg, mx_gemm_kernel<FMT, TILE, SUB, CG, ACT>, m, a);
 }
 
-template <int FMT, int TILE, int CG>
+template <int FMT, int TILE, int SUB, int CG>
 cudaError_t launch_act(const MxMaps &m, const MxGemmArgs &a, int num_sms, cudaStream_t s) {
-    if (a.out_f32) return launch<FMT, TILE, CG, kActRuntime>(m, a, num_sms, s);
+    if (a.out_f32) return launch<FMT, TILE, SUB, CG, kActRuntime>(m, a, num_sms, s);
     switch (a.act) {
-        case 0: return launch<FMT, TILE, CG, 0>(m, a, num_sms, s);
-        case 1: return launch<FMT, TILE, CG, 1>(m, a, num_sms, s);
-        case 2: return launch<FMT, TILE, CG, 2>(m, a, num_sms, s);
-        default: return launch<FMT, TILE, CG, -1>(m, a, num_sms, s);
+        case 0: return launch<FMT, TILE, SUB, CG, 0>(m, a, num_sms, s);
+        case 1: return launch<FMT, TILE, SUB, CG, 1>(m, a, num_sms, s);
+        case 2: return launch<FMT, TILE, SUB, CG, 2>(m, a, num_sms, s);
+        default: return launch<FMT, TILE, SUB, CG, -1>(m, a, num_sms, s);
     }
 }
 
@@ -450,8 +523,8 @@ cudaError_t launch_mx_gemm(const MxMaps &m, const MxGemmArgs &a, int format, int
     const int64_t filled = (int64_t)a.rows - (a.G > 1 ? (int64_t)a.G * 127 : 0);
     const bool narrow = filled <= (int64_t)64 * a.G;
     if (format == kMxFp4)
-        return narrow ? launch_act<kMxFp4, 64, 1>(m, a, num_sms, s) : launch_act<kMxFp4, 192, 2>(m, a, num_sms, s);
-    return narrow ? launch_act<kNvFp4, 64, 1>(m, a, num_sms, s) : launch_act<kNvFp4, 192, 2>(m, a, num_sms, s);
+        return narrow ? launch_act<kMxFp4, 64, 1, 1>(m, a, num_sms, s) : launch_act<kMxFp4, 192, 2, 2>(m, a, num_sms, s);
+    return narrow ? launch_act<kNvFp4, 64, 1, 1>(m, a, num_sms, s) : launch_act<kNvFp4, 192, 2, 2>(m, a, num_sms, s);
 }
 
 }  // namespace moe

@@ -11,15 +11,15 @@
 // NVFP4 divides fp32 elements (correctly rounded: a quotient that is not one of
 // the rounding borders cannot round onto one, as border times scale has at most
 // 7 significant bits). For bf16 elements the quotient times 1 / scale is off by
-// less than 2^-20, and is rounded to a multiple of 2^-12: borders (multiples of
+// less than 2^-19, and is rounded to a multiple of 2^-12: borders (multiples of
 // 1/4) come out exactly, and every other quotient is at least 2^-10 away from
 // one, since element and border times scale differ by 2^-8 of themselves.
 //
-// Bound by HBM: 2 (bf16) or 4 bytes are read and 0.5 + 1 / block written per
-// element. A thread takes 8 neighbouring elements, a warp 1024 of one row in
-// four steps whose loads are in flight together; the block's maximum is a
-// shuffle over 4 or 2 lanes, and the lanes of 4 blocks put their scale bytes
-// together into the one 32-bit word that the scale tile holds of them.
+// 2 (bf16) or 4 bytes are read and 0.5 + 1 / block written per element; the
+// instructions per element are what stands between that and HBM's rate, so a
+// thread takes 16 neighbouring elements (32-byte loads): one NVFP4 block or half
+// an MXFP4 one, whose scale it works out once; the lanes of 4 blocks put their
+// scale bytes together into the one 32-bit word that the scale tile holds of them.
 #include <algorithm>
 
 #include "mx_common.cuh"
@@ -28,27 +28,34 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSteps = 4;                 // steps of 256 elements a warp takes
-constexpr int kWarpElems = 256 * kSteps;  // elements of one row per warp
 
-// Two E2M1 codes, `lo` in the low four bits.
-__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
+// Eight E2M1 codes, the first in the low four bits.
+__device__ __forceinline__ uint32_t e2m1x8(const float *v) {
     uint32_t r;
-    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tcvt.u32.u8 %0, b;\n\t}"
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
         : "=r"(r)
-        : "f"(lo), "f"(hi));
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
     return r;
+}
+
+__device__ __forceinline__ float2 f16x2_values(uint32_t h) {
+    float lo, hi;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(h));
+    return make_float2(lo, hi);
 }
 
 // The values of two codes (fp16 holds them exactly), `x` the low one's.
 __device__ __forceinline__ float2 e2m1x2_values(uint32_t b) {
     uint32_t h;
     asm("{\n\t.reg .b8 b;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(h) : "r"(b));
-    float lo, hi;
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
-        : "=f"(lo), "=f"(hi)
-        : "r"(h));
-    return make_float2(lo, hi);
+    return f16x2_values(h);
 }
 
 // E4M3 byte of v >= 0, to nearest even, at most 448.
@@ -58,33 +65,82 @@ __device__ __forceinline__ uint32_t e4m3_of(float v) {
     return r & 0xffu;
 }
 
+// The value of an E4M3 byte that is not NaN (fp16 holds it exactly).
+__device__ __forceinline__ float e4m3_finite(uint32_t b) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(b)));
+    return f16x2_values(h).x;
+}
+
+__device__ __forceinline__ float rcp_approx(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ void load32(const void *p, uint32_t *w) {
+    asm("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+        : "l"(p));
+}
+
+__device__ __forceinline__ void store32(void *p, const uint32_t *w) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+constexpr int kLaneElems = 16;              // neighbouring elements of a row that a thread takes
+constexpr int kStep = 32 * kLaneElems;      // and a warp
+
+// Sixteen elements of a row as they lie in memory.
 template <typename XT>
-__device__ __forceinline__ void load8(const XT *p, bool vec, float (&v)[8]) {
-    if constexpr (sizeof(XT) == 2) {
-        if (vec) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p));
-            const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+struct Raw {
+    static constexpr int kWords = kLaneElems * sizeof(XT) / 4;
+    uint32_t w[kWords];
+};
+
+template <typename XT>
+__device__ __forceinline__ Raw<XT> load16(const XT *p, bool vec) {
+    Raw<XT> r;
+    if (vec) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[2 * i] = __uint_as_float(a[i] << 16);
-                v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
-            }
-            return;
-        }
-    } else {
-        if (vec) {
-            const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-            return;
-        }
+        for (int i = 0; i < Raw<XT>::kWords; i += 8) load32(reinterpret_cast<const uint32_t *>(p) + i, r.w + i);
+        return r;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_f32(p[i]);
+    for (int i = 0; i < kLaneElems; ++i) {
+        if constexpr (sizeof(XT) == 2) {
+            const uint32_t h = __bfloat16_as_ushort(p[i]);
+            r.w[i / 2] = i % 2 ? r.w[i / 2] | (h << 16) : h;
+        } else {
+            r.w[i] = __float_as_uint(p[i]);
+        }
+    }
+    return r;
+}
+
+// The bits of the largest magnitude, as an fp32's (a NaN is the largest).
+template <typename XT>
+__device__ __forceinline__ uint32_t top_bits(const Raw<XT> &r) {
+    constexpr uint32_t kMask = sizeof(XT) == 2 ? 0x7fff7fffu : 0x7fffffffu;
+    uint32_t m = r.w[0] & kMask;
+#pragma unroll
+    for (int i = 1; i < Raw<XT>::kWords; ++i) {
+        if constexpr (sizeof(XT) == 2) m = __vmaxu2(m, r.w[i] & kMask);
+        else m = max(m, r.w[i] & kMask);
+    }
+    return sizeof(XT) == 2 ? max(m << 16, m & 0xffff0000u) : m;
 }
 
 template <typename XT>
-__device__ __forceinline__ void store8(XT *p, bool vec, const float (&v)[8]) {
+__device__ __forceinline__ float element(const Raw<XT> &r, int i) {
+    if constexpr (sizeof(XT) == 2) return __uint_as_float(i % 2 ? r.w[i / 2] & 0xffff0000u : r.w[i / 2] << 16);
+    else return __uint_as_float(r.w[i]);
+}
+
+template <typename XT>
+__device__ __forceinline__ void store8(XT *p, bool vec, const float *v) {
     if (!vec) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) p[i] = from_f32<XT>(v[i]);
@@ -104,88 +160,123 @@ __device__ __forceinline__ void store8(XT *p, bool vec, const float (&v)[8]) {
     }
 }
 
-template <int FMT, typename XT>
-__global__ void __launch_bounds__(kThreads) mx_quantize_kernel(const MxQuantArgs a, bool vec, bool vec_values) {
-    constexpr int kLanes = MxFormat<FMT>::kBlock / 8;  // lanes per block
-    const int lane = threadIdx.x & 31;
-    const int per_row = (a.cols + kWarpElems - 1) / kWarpElems;
-    const int64_t item = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int r = static_cast<int>(item / per_row);
-    if (r >= a.rows) return;
-    const int src = a.row_index ? a.row_index[r] : r;
-    if (src < 0 || src >= a.x_rows) return;
-    const int c0 = static_cast<int>(item - (int64_t)r * per_row) * kWarpElems + lane * 8;
-    const XT *x = static_cast<const XT *>(a.x) + (int64_t)src * a.ld;
-    float v[kSteps][8];
+template <typename XT>
+__device__ __forceinline__ void store16(XT *p, bool vec, const float *v) {
+    if (!vec) {
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-        if (c0 + 256 * s < a.cols) {
-            load8<XT>(x + c0 + 256 * s, vec, v[s]);
+        for (int i = 0; i < kLaneElems; ++i) p[i] = from_f32<XT>(v[i]);
+        return;
+    }
+    uint32_t w[Raw<XT>::kWords];
+#pragma unroll
+    for (int i = 0; i < Raw<XT>::kWords; ++i) {
+        if constexpr (sizeof(XT) == 2) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&b);
         } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[s][i] = 0.f;
+            w[i] = __float_as_uint(v[i]);
         }
     }
-    const int SB = mx_scale_tiles(a.cols, MxFormat<FMT>::kBlock);
-    uint8_t *srow = a.scales + (int64_t)(r / 128) * SB * 512 + (r % 32) * 16 + (r % 128 / 32) * 4;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-        const int c = c0 + 256 * s;
-        if (c - lane * 8 >= a.cols) break;  // warp-uniform
-        uint32_t top = 0u;  // max |u| as bits: a NaN is the largest
+    for (int i = 0; i < Raw<XT>::kWords; i += 8) store32(reinterpret_cast<uint32_t *>(p) + i, w + i);
+}
+
+// Codes, scale byte and scale of the lane's 16 elements (see the head of this file).
+template <int FMT, typename XT, bool PRE>
+__device__ __forceinline__ uint2 quantize16(const Raw<XT> &v, float pre, uint32_t &byte, float &scale) {
+    uint32_t top = top_bits<XT>(v);
+    if constexpr (FMT == kMxFp4) top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    // A finite maximum may leave the range when the power of two comes out: it then counts as infinite.
+    if (PRE) top = __float_as_uint(__uint_as_float(top) * pre);
+    const bool finite = top < 0x7f800000u;
+    float u[kLaneElems];
+    if constexpr (FMT == kMxFp4) {
+        const int e = static_cast<int>(top >> 23) - 2;
+        byte = finite ? static_cast<uint32_t>(e > 0 ? e : 0) : 255u;
+        scale = e8m0_value(byte);
+        const float inv = __uint_as_float((254u - min(byte, 253u)) << 23);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            v[s][i] *= a.pre;
-            top = max(top, __float_as_uint(v[s][i]) & 0x7fffffffu);
-        }
+        for (int i = 0; i < kLaneElems; ++i) u[i] = PRE ? element<XT>(v, i) * pre * inv : element<XT>(v, i) * inv;
+    } else {
+        byte = finite ? e4m3_of(__fdiv_rn(__uint_as_float(top), 6.f)) : 0u;
+        scale = e4m3_finite(byte);
+        if constexpr (sizeof(XT) == 2) {
+            const float inv = scale > 0.f ? rcp_approx(scale) : 0.f;
+            constexpr float kSnap = 0x1.8p11f;  // adding it rounds to multiples of 2^-12
 #pragma unroll
-        for (int off = kLanes / 2; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-        const bool finite = top < 0x7f800000u;
-        uint32_t byte;
-        float scale;
-        if constexpr (FMT == kMxFp4) {
-            const int e = static_cast<int>(top >> 23) - 2;
-            byte = finite ? static_cast<uint32_t>(e > 0 ? e : 0) : 255u;
-            scale = e8m0_value(byte);
-            const float inv = __uint_as_float((254u - min(byte, 253u)) << 23);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[s][i] *= inv;
-        } else {
-            byte = finite ? e4m3_of(__fdiv_rn(__uint_as_float(top), 6.f)) : 0x7fu;
-            scale = e4m3_value(byte);
-            if constexpr (sizeof(XT) == 2) {
-                const float inv = scale > 0.f ? __frcp_rn(scale) : 0.f;
-                constexpr float kSnap = 0x1.8p11f;  // adding it rounds to multiples of 2^-12
-#pragma unroll
-                for (int i = 0; i < 8; ++i)  // a quotient that becomes 0 keeps its sign
-                    v[s][i] = copysignf(__fsub_rn(__fmaf_rn(v[s][i], inv, kSnap), kSnap), v[s][i]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[s][i] = scale > 0.f ? __fdiv_rn(v[s][i], scale) : 0.f;
+            for (int i = 0; i < kLaneElems; ++i) {  // a quotient that becomes 0 keeps its sign
+                const float e = PRE ? element<XT>(v, i) * pre : element<XT>(v, i);
+                u[i] = copysignf(__fsub_rn(__fmaf_rn(e, inv, kSnap), kSnap), e);
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kLaneElems; ++i)
+                u[i] = __fdiv_rn(PRE ? element<XT>(v, i) * pre : element<XT>(v, i), scale);
         }
-        uint32_t code = 0u;
-        if (finite && scale > 0.f) {
+    }
+    uint2 code = make_uint2(e2m1x8(u), e2m1x8(u + 8));
+    if (!finite || !(scale > 0.f)) code = make_uint2(0u, 0u);
+    if (FMT == kNvFp4 && !finite) {
+        byte = 0x7fu;
+        scale = __uint_as_float(0x7fffffffu);
+    }
+    return code;
+}
+
+// A block takes `rpb` (at most 32) output rows, its warps pieces of STEPS x 512
+// elements of those that have a source row. PRE: a power of two comes out first.
+template <int FMT, typename XT, int STEPS, bool PRE>
+__global__ void __launch_bounds__(kThreads) mx_quantize_kernel(const MxQuantArgs a, int rpb, bool vec, bool vec_values) {
+    constexpr int kWordLanes = MxFormat<FMT>::kTileK / kLaneElems;  // lanes of one word of 4 scales
+    const int lane = threadIdx.x & 31;
+    const int r0 = blockIdx.x * rpb;
+    int src_l = -1;  // lane l: the source row of output row r0 + l
+    if (lane < rpb && r0 + lane < a.rows) src_l = a.row_index ? a.row_index[r0 + lane] : r0 + lane;
+    const uint32_t live = __ballot_sync(0xffffffffu, src_l >= 0 && src_l < a.x_rows);
+    const int per_row = (a.cols + kStep * STEPS - 1) / (kStep * STEPS);
+    const int items = __popc(live) * per_row;
+    const int SB = mx_scale_tiles(a.cols, MxFormat<FMT>::kBlock);
+    for (int item = threadIdx.x >> 5; item < items; item += kThreads / 32) {
+        const int nth = item / per_row;
+        // The nth row with a source: the lane that has so many of them before it.
+        const int i = __ffs(__ballot_sync(0xffffffffu, (live >> lane & 1u) && __popc(live & ((1u << lane) - 1u)) == nth)) - 1;
+        const int r = r0 + i, c0 = (item - nth * per_row) * (kStep * STEPS) + lane * kLaneElems;
+        const XT *x = static_cast<const XT *>(a.x) + (int64_t)__shfl_sync(0xffffffffu, src_l, i) * a.ld + c0;
+        Raw<XT> v[STEPS];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) code |= e2m1x2(v[s][2 * i], v[s][2 * i + 1]) << (8 * i);
+        for (int s = 0; s < STEPS; ++s) {
+            if (c0 + kStep * s < a.cols) v[s] = load16<XT>(x + kStep * s, vec);
+            else v[s] = Raw<XT>{};
         }
-        uint32_t word = byte << (8 * (lane / kLanes & 3));
+        uint8_t *codes = a.codes + (int64_t)r * (a.cols / 2) + c0 / 2;
+        const int j = c0 / MxFormat<FMT>::kTileK;  // scale tile of this lane's block
+        uint8_t *tile = a.scales + ((int64_t)(r / 128) * SB + j) * 512 + (r % 32) * 16 + (r % 128 / 32) * 4;
 #pragma unroll
-        for (int off = kLanes; off < 4 * kLanes; off <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, off);
-        const int j = c / MxFormat<FMT>::kTileK;  // scale tile of this lane's block
-        if (lane % (4 * kLanes) == 0 && j < SB) *reinterpret_cast<uint32_t *>(srow + (int64_t)j * 512) = word;
-        if (c < a.cols) {
-            *reinterpret_cast<uint32_t *>(a.codes + (int64_t)r * (a.cols / 2) + c / 2) = code;
-            if (a.values) {
-                float o[8];
-                const float m = scale * a.post;
+        for (int s = 0; s < STEPS; ++s) {
+            const int c = c0 + kStep * s;
+            if (c - lane * kLaneElems >= a.cols) break;  // warp-uniform
+            uint32_t byte;
+            float scale;
+            const uint2 code = quantize16<FMT, XT, PRE>(v[s], a.pre, byte, scale);
+            constexpr int kBlockLanes = kWordLanes / 4;
+            uint32_t word = byte << (8 * (lane / kBlockLanes & 3));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 q = e2m1x2_values(code >> (8 * i) & 0xffu);
-                    o[2 * i] = q.x * m;
-                    o[2 * i + 1] = q.y * m;
+            for (int off = kBlockLanes; off < kWordLanes; off <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, off);
+            if (lane % kWordLanes == 0 && j + kStep / MxFormat<FMT>::kTileK * s < SB)
+                *reinterpret_cast<uint32_t *>(tile + kStep / MxFormat<FMT>::kTileK * 512 * s) = word;
+            if (c < a.cols) {
+                *reinterpret_cast<uint2 *>(codes + kStep / 2 * s) = code;
+                if (a.values) {
+                    float o[kLaneElems];
+                    const float m = scale * a.post;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 q = e2m1x2_values((i < 4 ? code.x : code.y) >> (8 * (i % 4)) & 0xffu);
+                        o[2 * i] = q.x * m;
+                        o[2 * i + 1] = q.y * m;
+                    }
+                    store16<XT>(static_cast<XT *>(a.values) + (int64_t)r * a.values_ld + c, vec_values, o);
                 }
-                store8<XT>(static_cast<XT *>(a.values) + (int64_t)r * a.values_ld + c, vec_values, o);
             }
         }
     }
@@ -212,17 +303,20 @@ __global__ void __launch_bounds__(kThreads) mx_dequantize_kernel(const MxDequant
     store8<OT>(static_cast<OT *>(a.out) + r * a.ld + c, vec, o);
 }
 
-bool vector_rows(const void *p, int64_t ld, int elem) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * elem % 16 == 0;
+bool vector_rows(const void *p, int64_t ld, int elem, int bytes) {
+    return reinterpret_cast<uintptr_t>(p) % bytes == 0 && ld * elem % bytes == 0;
 }
 
-template <int FMT, typename XT>
-cudaError_t quantize(const MxQuantArgs &a, cudaStream_t s) {
-    const int64_t items = (int64_t)a.rows * ((a.cols + kWarpElems - 1) / kWarpElems);
-    const int64_t blocks = (items + kThreads / 32 - 1) / (kThreads / 32);
-    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-    mx_quantize_kernel<FMT, XT><<<(int)blocks, kThreads, 0, s>>>(a, vector_rows(a.x, a.ld, sizeof(XT)),
-                                                                 vector_rows(a.values, a.values_ld, sizeof(XT)));
+template <int FMT, typename XT, int STEPS>
+cudaError_t quantize(const MxQuantArgs &a, int num_sms, cudaStream_t s) {
+    const int64_t items = (int64_t)a.rows * ((a.cols + kStep * STEPS - 1) / (kStep * STEPS));
+    // Rows per block: one piece for each warp, and no more blocks than 64 for each SM.
+    int rpb = 1;
+    while (rpb < 32 && ((int64_t)rpb * items < (int64_t)a.rows * (kThreads / 32) || a.rows / rpb > 64 * num_sms)) rpb *= 2;
+    const int blocks = (a.rows + rpb - 1) / rpb;
+    const bool vec = vector_rows(a.x, a.ld, sizeof(XT), 32), vv = vector_rows(a.values, a.values_ld, sizeof(XT), 32);
+    if (a.pre != 1.f) mx_quantize_kernel<FMT, XT, STEPS, true><<<blocks, kThreads, 0, s>>>(a, rpb, vec, vv);
+    else mx_quantize_kernel<FMT, XT, STEPS, false><<<blocks, kThreads, 0, s>>>(a, rpb, vec, vv);
     return cudaGetLastError();
 }
 
@@ -230,15 +324,16 @@ template <int FMT, typename OT>
 cudaError_t dequantize(const MxDequantArgs &a, cudaStream_t s) {
     const int64_t blocks = ((int64_t)a.rows * (a.cols / 8) + kThreads - 1) / kThreads;
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-    mx_dequantize_kernel<FMT, OT><<<(int)blocks, kThreads, 0, s>>>(a, vector_rows(a.out, a.ld, sizeof(OT)));
+    mx_dequantize_kernel<FMT, OT><<<(int)blocks, kThreads, 0, s>>>(a, vector_rows(a.out, a.ld, sizeof(OT), 16));
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_mx_quantize(const MxQuantArgs &a, int format, bool bf16, cudaStream_t s) {
-    if (format == kMxFp4) return bf16 ? quantize<kMxFp4, __nv_bfloat16>(a, s) : quantize<kMxFp4, float>(a, s);
-    return bf16 ? quantize<kNvFp4, __nv_bfloat16>(a, s) : quantize<kNvFp4, float>(a, s);
+cudaError_t launch_mx_quantize(const MxQuantArgs &a, int format, bool bf16, int num_sms, cudaStream_t s) {
+    if (format == kMxFp4)
+        return bf16 ? quantize<kMxFp4, __nv_bfloat16, 2>(a, num_sms, s) : quantize<kMxFp4, float, 1>(a, num_sms, s);
+    return bf16 ? quantize<kNvFp4, __nv_bfloat16, 2>(a, num_sms, s) : quantize<kNvFp4, float, 1>(a, num_sms, s);
 }
 
 cudaError_t launch_mx_dequantize(const MxDequantArgs &a, int format, bool bf16, cudaStream_t s) {

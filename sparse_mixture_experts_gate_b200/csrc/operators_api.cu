@@ -238,7 +238,7 @@ int moe_mx_quantize(int32_t format, const void *x, int32_t dtype, int64_t ld, in
     a.values = values;
     a.values_ld = values_ld;
     a.post = std::ldexp(1.f, scale_exp);
-    return launched(launch_mx_quantize(a, format, dtype == MOE_DTYPE_BF16, as_stream(stream_v)), "moe_mx_quantize");
+    return launched(launch_mx_quantize(a, format, dtype == MOE_DTYPE_BF16, sms, as_stream(stream_v)), "moe_mx_quantize");
 }
 
 int moe_mx_dequantize(int32_t format, const void *codes, const void *scales, int32_t rows, int32_t cols,
@@ -305,6 +305,7 @@ int moe_mx_gemm(const moe_mx_gemm_t *p, void *stream_v) {
     const uint64_t tiles = mx_scale_tiles(p->k, block_of(p->format));
     if (!encode_u8_2d(&m.w, p->w_codes, p->k / 2, (uint64_t)p->groups * p->n, 128) ||
         !encode_u8_2d(&m.a, p->a_codes, p->k / 2, p->rows, 16) ||
+        !encode_u8_2d(&m.a96, p->a_codes, p->k / 2, p->rows, 96) ||
         !encode_scale_tiles(&m.sw, p->w_scales, tiles, (uint64_t)p->groups * ((p->n + 127) / 128),
                             256 / (4 * block_of(p->format))) ||
         !encode_scale_tiles(&m.sa, p->a_scales, tiles, ((uint64_t)p->rows + 127) / 128, 256 / (4 * block_of(p->format))))

@@ -77,21 +77,29 @@ enum : uint32_t { kDevBadGroup = 2u };
 
 // ------------------------------------------------------------------ tcgen05
 
-// Shared-memory descriptor of one 512-byte scale tile (32 rows of 16 bytes, no
-// swizzle, 8-row groups 128 bytes apart) for tcgen05.cp.32x128b.
-__device__ __forceinline__ uint64_t scale_tile_desc(uint32_t smem_addr) {
-    return static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 16) |
-           (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
-}
+// Shared-memory descriptors as two words: the low one holds address >> 4 in
+// bits [0,14) and the leading byte offset >> 4 in [16,30), so that a step through
+// shared memory (below 256 KB) is an addition to it; the high one is constant.
+// Operand tiles: K-major, 128B swizzle (see sw128_kmajor_desc).
+constexpr uint32_t kOperandDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t operand_desc_lo(uint32_t smem_addr) { return (smem_addr >> 4) | (1u << 16); }
+// A 512-byte scale tile (32 rows of 16 bytes, no swizzle, 8-row groups 128
+// bytes apart) for tcgen05.cp.32x128b.
+constexpr uint32_t kScaleDescHi = (128u >> 4) | (1u << 14);
+__device__ __forceinline__ uint32_t scale_desc_lo(uint32_t smem_addr) { return (smem_addr >> 4) | ((128u >> 4) << 16); }
 
 // Copies a scale tile into 4 TMEM columns (32 lanes, repeated in the four lane
 // quarters). Executes in order with the MMAs this thread issues after it.
 template <int CG>
-__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t desc) {
+__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint32_t desc_lo) {
     if constexpr (CG == 1)
-        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+        asm volatile("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+                     "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr), "r"(desc_lo), "n"(kScaleDescHi)
+                     : "memory");
     else
-        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+        asm volatile("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+                     "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr), "r"(desc_lo), "n"(kScaleDescHi)
+                     : "memory");
 }
 
 // Instruction descriptor of kind::mxf4 / kind::mxf4nvf4 with E2M1 operands,
@@ -109,15 +117,16 @@ __host__ __device__ constexpr uint32_t mx_idesc_sf(uint32_t id) { return (id << 
 
 // D[tmem] (+)= (A * scale_a) (B * scale_b)^T over 64 elements of K.
 template <int FMT, int CG>
-__device__ __forceinline__ void tc_mma_mx(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+__device__ __forceinline__ void tc_mma_mx(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t sfa,
+                                          uint32_t sfb, uint32_t accumulate) {
 #define MOE_MX_MMA(KIND, CGS, VEC)                                                                            \
     asm volatile(                                                                                             \
-        "{\n\t.reg .pred p;\n\t"                                                                              \
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"                                                          \
         "setp.ne.b32 p, %6, 0;\n\t"                                                                           \
+        "mov.b64 a, {%1, %7};\n\tmov.b64 b, {%2, %7};\n\t"                                                    \
         "tcgen05.mma.cta_group::" CGS ".kind::" KIND ".block_scale.scale_vec::" VEC                           \
-        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),                                               \
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)                             \
+        " [%0], a, b, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),                                                \
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "n"(kOperandDescHi)            \
         : "memory")
     if constexpr (FMT == kMxFp4 && CG == 1) MOE_MX_MMA("mxf4", "1", "2X");
     if constexpr (FMT == kMxFp4 && CG == 2) MOE_MX_MMA("mxf4", "2", "2X");

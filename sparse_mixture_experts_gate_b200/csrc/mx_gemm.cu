@@ -282,31 +282,57 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ MMA (leader)
         if (leader) {
             const bool one = elect_one();
-            uint32_t it = 0, uses[SUB] = {}, tcount = 0;
+            const uint32_t w_lo = operand_desc_lo(smem_u32(sW)), t_lo = operand_desc_lo(smem_u32(sT));
+            const uint32_t sw_lo = scale_desc_lo(smem_u32(sSfW)), st_lo = scale_desc_lo(smem_u32(sSfT));
+            uint32_t uses[SUB] = {}, tcount = 0;
+            uint32_t st = 0, ph = 0;              // stage and its parity
+            uint32_t buf = 0, old = 0, old_ph = 0;  // scale buffer; the stage that used it last, and its parity
+            bool reused = false;
             for (int u = first; u < total && ok; u += step, ++tcount) {
                 const Unit w = unit_of(u);
                 const int nrb = (w.row0 % 128 + w.ntok + 127) / 128;
                 const uint32_t shift = (w.row0 % 128) / 32;  // first scale column of the unit's tokens
-                int cols[SUB];
+                uint32_t idesc[SUB];  // 0: no tokens
 #pragma unroll
-                for (int s = 0; s < SUB; ++s)
-                    cols[s] = (min(TILE, max(w.ntok - s * TILE, 0)) + C::kStep - 1) / C::kStep * C::kStep;
-                for (int kb = 0; kb < kblocks && ok; ++kb, ++it) {
-                    const int st = it % kStages;
-                    // The MMAs that read this scale buffer before are done.
-                    if (C::kSfBufs < kStages && it >= C::kSfBufs)
-                        ok = mbar_wait(&empty[(it - C::kSfBufs) % kStages], ((it - C::kSfBufs) / kStages) & 1u, status);
-                    if (ok) ok = mbar_wait(&full[st], (it / kStages) & 1u, status);
+                for (int s = 0; s < SUB; ++s) {
+                    const int cols = (min(TILE, max(w.ntok - s * TILE, 0)) + C::kStep - 1) / C::kStep * C::kStep;
+                    idesc[s] = cols ? mx_idesc<FMT>(kFeat * CG, cols) : 0u;
+                }
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    if constexpr (C::kSfBufs < kStages) {  // the MMAs that read this scale buffer before are done
+                        if (reused) ok = mbar_wait(&empty[old], old_ph, status);
+                    }
+                    if (ok) ok = mbar_wait(&full[st], ph, status);
+                    if (kb == 0 && ok) {  // the (first) accumulator has been drained
+                        const uint32_t use = SUB == 2 ? uses[0] : tcount >> 1;
+                        ok = mbar_wait(&tempty[SUB == 2 ? 0 : tcount & 1u], (use & 1u) ^ 1u, status);
+                        ++uses[0];
+                    }
                     if (!__all_sync(0xffffffffu, ok)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after_sync();
-                    const uint32_t sfa = tmem_base + C::kScaleCol + (it % C::kSfBufs) * C::kSfCols;
-                    const uint32_t sfb = sfa + C::kSfColsA;
+                    const uint32_t sfa = tmem_base + C::kScaleCol + buf * C::kSfCols, sfb = sfa + C::kSfColsA;
+                    const bool last = kb == kblocks - 1;
+                    const int steps = last ? (a.K - kb * kStageK + 63) / 64 : 4;
+                    auto products = [&](int s) {
+                        const uint32_t acc = SUB == 2 ? s : tcount & 1u;
+                        const uint32_t al = w_lo + st * (kWBytes >> 4), bl = t_lo + st * (C::kB >> 4) + s * (C::kSub >> 4);
+                        const uint32_t d = tmem_base + acc * TILE, sb = sfb + shift + s * (TILE / 32);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            if (kk >= steps) break;
+                            // 64 elements: half of an MXFP4 scale tile's 4 scales, a whole NVFP4 one's.
+                            const int j = FMT == kMxFp4 ? kk / 2 : kk;
+                            const uint32_t id = FMT == kMxFp4 ? 2u * (kk & 1) : 0u;
+                            tc_mma_mx<FMT, CG>(d, al + 2u * kk, bl + 2u * kk, idesc[s] | mx_idesc_sf(id), sfa + 4 * j,
+                                               sb + j * C::kRowBlocks * 4, kk > 0 ? 1u : (kb > 0 ? 1u : 0u));
+                        }
+                        if (last) commit_all(&tfull[acc]);
+                    };
                     if (one) {
-                        const uint64_t da = scale_tile_desc(smem_u32(sSfW + st * C::kSfA));
-                        const uint64_t db = scale_tile_desc(smem_u32(sSfT + st * C::kSfB));
+                        const uint32_t da = sw_lo + st * (C::kSfA >> 4), db = st_lo + st * (C::kSfB >> 4);
 #pragma unroll
                         for (int j = 0; j < C::kSfTiles; ++j) {
                             tc_cp_scales<CG>(sfa + 4 * j, da + 32u * j);
@@ -315,40 +341,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (b < nrb)
                                     tc_cp_scales<CG>(sfb + (j * C::kRowBlocks + b) * 4, db + 32u * (b * C::kSfTiles + j));
                         }
+                        products(0);
                     }
-                    const int steps = (min(kStageK, a.K - kb * kStageK) + 63) / 64;
-#pragma unroll
-                    for (int s = 0; s < SUB; ++s) {
-                        if (cols[s] == 0) continue;
-                        const uint32_t acc = SUB == 2 ? s : tcount & 1u;
-                        if (kb == 0) {  // the accumulator has been drained
-                            const uint32_t use = SUB == 2 ? uses[s] : tcount >> 1;
-                            if (!__all_sync(0xffffffffu, mbar_wait(&tempty[acc], (use & 1u) ^ 1u, status))) {
+                    if (SUB == 2 && idesc[SUB - 1]) {
+                        if (kb == 0) {
+                            if (!__all_sync(0xffffffffu, mbar_wait(&tempty[SUB - 1], (uses[SUB - 1] & 1u) ^ 1u, status))) {
                                 ok = false;
                                 break;
                             }
-                            ++uses[s];
+                            ++uses[SUB - 1];
                             tc_fence_after_sync();
                         }
-                        if (one) {
-                            const uint32_t idesc = mx_idesc<FMT>(kFeat * CG, cols[s]);
-                            const uint64_t ad = sw128_kmajor_desc(smem_u32(sW + st * kWBytes));
-                            const uint64_t bd = sw128_kmajor_desc(smem_u32(sT + st * C::kB + s * C::kSub));
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) {
-                                if (kk >= steps) break;
-                                // 64 elements: half of an MXFP4 scale tile's 4 scales, a whole NVFP4 one's.
-                                const int j = FMT == kMxFp4 ? kk / 2 : kk;
-                                const uint32_t id = FMT == kMxFp4 ? 2u * (kk & 1) : 0u;
-                                tc_mma_mx<FMT, CG>(tmem_base + acc * TILE, ad + 2u * kk, bd + 2u * kk,
-                                                   idesc | mx_idesc_sf(id), sfa + 4 * j,
-                                                   sfb + j * C::kRowBlocks * 4 + shift + s * (TILE / 32),
-                                                   (kb | kk) != 0 ? 1u : 0u);
-                            }
-                            if (kb == kblocks - 1) commit_all(&tfull[acc]);
-                        }
+                        if (one) products(SUB - 1);
                     }
-                    if (ok && one) commit_all(&empty[st]);
+                    if (one) commit_all(&empty[st]);
+                    if constexpr (C::kSfBufs < kStages) {
+                        if (reused && ++old == kStages) {
+                            old = 0;
+                            old_ph ^= 1u;
+                        }
+                        if (++buf == C::kSfBufs) {
+                            buf = 0;
+                            reused = true;
+                        }
+                    } else {
+                        buf = st + 1 == kStages ? 0 : st + 1;
+                    }
+                    if (++st == kStages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
                     __syncwarp();
                 }
             }

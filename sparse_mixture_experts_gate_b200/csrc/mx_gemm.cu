@@ -18,11 +18,11 @@
 // expert) are bound by the weights' bytes: single CTAs, 128 features x up to 64
 // tokens, a deeper pipeline, two accumulators in turn.
 //
-// Per CTA (320 threads): warp 0 loads codes (TMA, 128B swizzle, 256 elements
+// Per CTA (576 threads): warp 0 loads codes (TMA, 128B swizzle, 256 elements
 // of K a stage) and scale tiles, signalling the (leader's) stage barrier; warp
 // 1 owns TMEM and, in the leader, copies a stage's scale tiles into TMEM
-// (tcgen05.cp, both CTAs') and issues its MMAs; warps 2..9 drain this CTA's 128
-// features of the accumulators, two warps for each quarter of the TMEM lanes. The
+// (tcgen05.cp, both CTAs') and issues its MMAs; warps 2..17 drain this CTA's 128
+// features of the accumulators, four warps for each quarter of the TMEM lanes. The
 // loading and issuing warps run their loops with all lanes and elect one only for
 // the instructions themselves: descriptors then stay in uniform registers (with
 // one lane in the loop, issuing took longer than the products: 121 us instead of
@@ -36,7 +36,7 @@
 //
 // Epilogue of bf16 outputs: TMEM is read in 16 x 256-bit pieces, whose register
 // layout (a lane holds two neighbouring tokens of one feature) is the one that
-// stmatrix.trans takes, so a warp turns 32 tokens x 32 features around through a
+// stmatrix.trans takes, so a warp turns 16 tokens x 32 features around through a
 // shared buffer of its own without shuffles, and stores each token's 64 bytes
 // with 16-byte stores. A warp takes all of its part of an accumulator into
 // registers and hands the accumulator back before it computes. fp32 outputs are
@@ -51,15 +51,14 @@
 namespace moe {
 namespace {
 
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;               // four for each quarter of the TMEM lanes
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kFeat = 128;                // features per CTA
 constexpr int kStageK = 256;              // elements of K per stage: 128 bytes of codes
 constexpr int kWBytes = kFeat * 128;      // weight codes per stage
 constexpr int kMaxGroups = 1024;
 constexpr int kTmemCols = 512;
-constexpr int kPitch = 80;                // bytes of a staged token row (64 used): conflict-free stmatrix
-constexpr int kStageOut = 32 * kPitch;    // one warp's output buffer
+constexpr int kStageOut = 16 * 64;        // one warp's output buffer: 16 tokens x 32 bf16 features
 constexpr int kActRuntime = -2;           // fp32 outputs: the activation is looked up at run time
 
 // TILE tokens per accumulator, SUB accumulators per unit.
@@ -84,6 +83,7 @@ struct Cfg {
     static constexpr int kSfBufs = kSfFit < kStages ? kSfFit : kStages;
     static constexpr int kStep = 16 * CG;                             // token rows: a TMA box per CTA
     static_assert(kStages >= 4 && kSfBufs >= 2, "pipeline depth");
+    static_assert(TILE % 64 == 0 && kEpiWarps == 16, "the epilogue warps share an accumulator evenly");
     static_assert(SUB == 1 || kUnitTok % 128 == 0, "units start on a scale tile");
     static_assert(kSub % 1024 == 0, "operand tiles keep the 1024-byte swizzle alignment");
 };
@@ -99,14 +99,25 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0u;
 }
 
-__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+// Byte of 16-byte piece p (0..3) of token row r in a warp's output buffer: pieces
+// trade places by row, so that eight rows' pieces p (stmatrix) as well as two
+// rows' four pieces (the loads that follow) lie in different banks.
+__device__ __forceinline__ int staged(int r, int p) { return r * 64 + ((p ^ (r >> 1 & 3)) << 4); }
+
+// Arrives on an mbarrier of either CTA of the pair with CTA-scope release. What
+// it hands over is the accumulator, whose loads have completed (wait::ld, then the
+// tcgen05 fence); a cluster-scope release would also wait for this thread's
+// earlier output stores to land (with it, 147 instead of 103 us for 64 experts,
+// 49152 rows, 1408 x 2048, NVFP4, swish).
+__device__ __forceinline__ void arrive_pair(uint32_t bar_cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster_addr) : "memory");
 }
 
 // Four 8 x 8 matrices of 16-bit values, transposed: lane 8 m + i gives the address of row i of matrix m.
@@ -130,8 +141,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *empty = full + kStages, *tfull = empty + kStages, *tempty = tfull + 2, *mma_done = tempty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
     uint32_t *status = tmem_slot + 1;
-    int32_t *scan = reinterpret_cast<int32_t *>(tmem_slot + 2);    // [16]
-    int32_t *prefix = scan + 16;                                   // [G + 1] token tiles before each group
+    int32_t *scan = reinterpret_cast<int32_t *>(tmem_slot + 2);    // [32]
+    int32_t *prefix = scan + 32;                                   // [G + 1] token tiles before each group
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
     const bool leader = rank == 0;
@@ -384,14 +395,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;             // the TMEM lane quarter this warp may read
-        const int half = (warp - 2) >> 2;   // which of the quarter's two warps: every other 32 tokens
+        const int part = (warp - 2) >> 2;   // which of the quarter's four warps: every fourth 16 tokens
         const uint8_t *own = sOut + (warp - 2) * kStageOut;
         const uint32_t buf = smem_u32(own);
         auto release = [&](uint32_t acc) {
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) {
-                if constexpr (CG == 2) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
+                if constexpr (CG == 2) arrive_pair(mapa_shared(smem_u32(&tempty[acc]), 0));
                 else mbar_arrive(&tempty[acc]);
             }
         };
@@ -421,12 +432,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * TILE;
                 if constexpr (ACT != kActRuntime) {
                     constexpr int kChunks = TILE / 64;
-                    uint32_t lo[kChunks][16], hi[kChunks][16];  // features 0..15 and 16..31 of the quarter
+                    uint32_t lo[kChunks][8], hi[kChunks][8];  // features 0..15 and 16..31 of the quarter
 #pragma unroll
                     for (int i = 0; i < kChunks; ++i) {
-                        if (half * 32 + 64 * i < ntok) {
-                            tmem_ld_16x256b_x4(taddr + half * 32 + 64 * i, lo[i]);
-                            tmem_ld_16x256b_x4(taddr + (16u << 16) + half * 32 + 64 * i, hi[i]);
+                        const int c = part * 16 + 64 * i;
+                        if (c < ntok) {
+                            tmem_ld_16x256b_x2(taddr + c, lo[i]);
+                            tmem_ld_16x256b_x2(taddr + (16u << 16) + c, hi[i]);
                         }
                     }
                     tmem_ld_wait();
@@ -437,43 +449,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                   activate_t<ACT>(fmaf(__uint_as_float(y), mul, b)));
                         return *reinterpret_cast<const uint32_t *>(&p);
                     };
+                    const int f = f0 + lane % 4 * 8;
+                    __nv_bfloat16 *orow = static_cast<__nv_bfloat16 *>(a.out) +
+                                          (int64_t)(row0 + part * 16 + lane / 4) * a.out_ld + f;
+                    const bool whole = a.vec_ok && f + 8 <= a.N;
 #pragma unroll
                     for (int i = 0; i < kChunks; ++i) {
-                        const int c = half * 32 + 64 * i;
+                        const int c = part * 16 + 64 * i;
                         if (c >= ntok) break;
+                        uint32_t pk[8];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            stmatrix_x4_trans(buf + (8 * j + lane % 8) * kPitch + lane / 8 * 16,
-                                              pack(lo[i][4 * j], lo[i][4 * j + 1], bv[0]),
-                                              pack(lo[i][4 * j + 2], lo[i][4 * j + 3], bv[1]),
-                                              pack(hi[i][4 * j], hi[i][4 * j + 1], bv[2]),
-                                              pack(hi[i][4 * j + 2], hi[i][4 * j + 3], bv[3]));
+                        for (int j = 0; j < 2; ++j) {
+                            pk[4 * j] = pack(lo[i][4 * j], lo[i][4 * j + 1], bv[0]);
+                            pk[4 * j + 1] = pack(lo[i][4 * j + 2], lo[i][4 * j + 3], bv[1]);
+                            pk[4 * j + 2] = pack(hi[i][4 * j], hi[i][4 * j + 1], bv[2]);
+                            pk[4 * j + 3] = pack(hi[i][4 * j + 2], hi[i][4 * j + 3], bv[3]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            stmatrix_x4_trans(buf + staged(8 * j + lane % 8, lane / 8), pk[4 * j], pk[4 * j + 1],
+                                              pk[4 * j + 2], pk[4 * j + 3]);
                         __syncwarp();
-                        const int f = f0 + lane % 4 * 8;
+                        uint4 v[2];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int t = c + 8 * k + lane / 4;
-                            const uint4 v =
-                                *reinterpret_cast<const uint4 *>(own + (8 * k + lane / 4) * kPitch + lane % 4 * 16);
-                            if (t < ntok && f < a.N) {
-                                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.out) + (int64_t)(row0 + t) * a.out_ld + f;
-                                if (a.vec_ok && f + 8 <= a.N) {
-                                    *reinterpret_cast<uint4 *>(o) = v;
-                                } else {
-                                    const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+                        for (int k = 0; k < 2; ++k)
+                            v[k] = *reinterpret_cast<const uint4 *>(own + staged(8 * k + lane / 4, lane % 4));
+                        __syncwarp();
 #pragma unroll
-                                    for (int e = 0; e < 8; ++e)
-                                        if (f + e < a.N)
-                                            o[e] = __ushort_as_bfloat16(
-                                                static_cast<unsigned short>(words[e / 2] >> (16 * (e & 1))));
-                                }
+                        for (int k = 0; k < 2; ++k) {
+                            if (c + 8 * k + lane / 4 >= ntok) continue;
+                            __nv_bfloat16 *o = orow + (64 * i + 8 * k) * a.out_ld;
+                            if (whole) {
+                                *reinterpret_cast<uint4 *>(o) = v[k];
+                            } else {
+                                const uint32_t words[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    if (f + e < a.N)
+                                        o[e] = __ushort_as_bfloat16(
+                                            static_cast<unsigned short>(words[e / 2] >> (16 * (e & 1))));
                             }
                         }
-                        __syncwarp();
                     }
                 } else {
                     const int f = f0 + lane;
-                    for (int c = half * 16; c < ntok; c += 32) {
+                    for (int c = part * 16; c < ntok; c += 64) {
                         uint32_t r[16];
                         tmem_ld_32x32b_x16(taddr + c, r);
                         tmem_ld_wait();

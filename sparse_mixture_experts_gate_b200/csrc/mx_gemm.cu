@@ -11,12 +11,14 @@
 // columns. Unit = (token tile, feature tile); every CTA builds the groups' tile
 // prefix in shared memory and takes its share of the units in steps of the grid.
 //
-// Two forms. Long segments are bound by the operands' way from L2 (about 10 TB/s
-// here), so they run on CTA pairs (cta_group::2) whose unit is 256 features x 384
-// tokens, as two MMAs of 192 tokens into one accumulator each: each CTA stages its
-// 128 weight rows and half of the tokens. Short segments (a few tokens for each
-// expert) are bound by the weights' bytes: single CTAs, 128 features x up to 64
-// tokens, a deeper pipeline, two accumulators in turn.
+// Three forms (launch_mx_gemm has the rule). Long segments run on CTA pairs
+// (cta_group::2), 256 features x 192 tokens an accumulator, each CTA staging its
+// 128 weight rows and half of the tokens: either a unit fills both accumulators (384
+// tokens: the weights' way through L2 and shared memory is shared by twice the
+// tokens, but the next unit waits for the epilogue), or units take the two in turn
+// (the epilogue is hidden). Short segments (a few tokens for each expert) are bound
+// by the weights' bytes: single CTAs, 128 features x up to 64 tokens, a deeper
+// pipeline, two accumulators in turn.
 //
 // Per CTA (576 threads): warp 0 loads codes (TMA, 128B swizzle, 256 elements
 // of K a stage) and scale tiles, signalling the (leader's) stage barrier; warp
@@ -561,12 +563,19 @@ cudaError_t launch_act(const MxMaps &m, const MxGemmArgs &a, int num_sms, cudaSt
 }  // namespace
 
 cudaError_t launch_mx_gemm(const MxMaps &m, const MxGemmArgs &a, int format, int num_sms, cudaStream_t s) {
-    // Short segments: rows beyond the 127 that each group's start may leave unused.
+    // Short segments: rows beyond the 127 that each group's start may leave unused. With few rows a
+    // group the narrow form is far ahead (128 experts, 1024 rows, K 4096, N 1536: 81 us against 100).
     const int64_t filled = (int64_t)a.rows - (a.G > 1 ? (int64_t)a.G * 127 : 0);
     const bool narrow = filled <= (int64_t)64 * a.G;
+    // Both accumulators a unit from K = 4096 on: 223 us instead of 250 at K = 7168 (32 experts, 32768
+    // rows, N 2048), where the epilogue is short beside the products; 123 instead of 113 at K = 2048
+    // (64 experts, 49152 rows, N 1408).
+    const bool deep = a.K >= 4096;
     if (format == kMxFp4)
-        return narrow ? launch_act<kMxFp4, 64, 1, 1>(m, a, num_sms, s) : launch_act<kMxFp4, 192, 2, 2>(m, a, num_sms, s);
-    return narrow ? launch_act<kNvFp4, 64, 1, 1>(m, a, num_sms, s) : launch_act<kNvFp4, 192, 2, 2>(m, a, num_sms, s);
+        return narrow ? launch_act<kMxFp4, 64, 1, 1>(m, a, num_sms, s)
+                      : deep ? launch_act<kMxFp4, 192, 2, 2>(m, a, num_sms, s) : launch_act<kMxFp4, 192, 1, 2>(m, a, num_sms, s);
+    return narrow ? launch_act<kNvFp4, 64, 1, 1>(m, a, num_sms, s)
+                  : deep ? launch_act<kNvFp4, 192, 2, 2>(m, a, num_sms, s) : launch_act<kNvFp4, 192, 1, 2>(m, a, num_sms, s);
 }
 
 }  // namespace moe

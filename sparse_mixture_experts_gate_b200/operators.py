@@ -17,25 +17,20 @@ from . import binding as B
 
 _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
 _BLOCK = {"mxfp4": 32, "nvfp4": 16}
-
-
-def _ptr(t) -> Optional[int]:
-    return None if t is None else t.data_ptr()
-
-
-def _on(t: torch.Tensor):
-    """The raw current stream of t's device; the call has to run with that device current."""
-    return torch.cuda.current_stream(t.device).cuda_stream
+_current_device = torch.cuda.current_device
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    lambda device: torch.cuda.current_stream(device).cuda_stream
 
 
 def _call(t: torch.Tensor, fn, *args):
-    """fn(*args, stream) with t's device current."""
-    if not t.is_cuda:
+    """fn(*args, the current stream of t's device) with that device current."""
+    device = t.device.index
+    if device is None or not t.is_cuda:
         raise ValueError("the operators take CUDA tensors")
-    if t.device.index == torch.cuda.current_device():
-        return fn(*args, _on(t))
-    with torch.cuda.device(t.device):
-        return fn(*args, _on(t))
+    if device == _current_device():
+        return fn(*args, _raw_stream(device))
+    with torch.cuda.device(device):
+        return fn(*args, _raw_stream(device))
 
 
 def _rows(name: str, t: torch.Tensor, cols: Optional[int] = None) -> int:
@@ -45,18 +40,19 @@ def _rows(name: str, t: torch.Tensor, cols: Optional[int] = None) -> int:
                          f"got {tuple(t.shape)}")
     if t.dtype not in _DTYPE:
         raise ValueError(f"{name}: bf16 or fp32, got {t.dtype}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, width = t.shape
+    ld, inner = t.stride()
+    if inner != 1 and width > 1:
         raise ValueError(f"{name}: rows have to be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return ld if rows > 1 and ld >= width else (width if rows <= 1 else ld)
 
 
-def _array(name: str, t: Optional[torch.Tensor], like: torch.Tensor, dtype, shape=None):
-    if t is None:
-        return
-    if t.dtype != dtype or not t.is_contiguous() or t.device != like.device or \
-            (shape is not None and tuple(t.shape) != tuple(shape)):
+def _array(name: str, t: torch.Tensor, like: torch.Tensor, dtype, shape=None) -> int:
+    """The address of a contiguous array."""
+    if t.dtype != dtype or not t.is_contiguous() or t.device != like.device or (shape is not None and t.shape != shape):
         raise ValueError(f"{name}: a contiguous {dtype} tensor{'' if shape is None else f' of {tuple(shape)}'} on "
                          f"{like.device} is needed, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
 class RouteConfig:
@@ -78,20 +74,22 @@ def route(logits: torch.Tensor, cfg: RouteConfig, bias: Optional[torch.Tensor] =
     """Routes the tokens of logits [T][E] (bf16 or fp32). Returns (weights [T][k] fp32,
     topk_idx [T][k] int32, selections per expert [E] int32 or None); `out`: these
     three to write into. bias [E] fp32 takes part in the selection only."""
-    ld = _rows("logits", logits, cfg.num_experts)
-    T, E, k = logits.shape[0], cfg.num_experts, cfg.num_active
-    if bias is not None:
-        _array("bias", bias, logits, torch.float32, (E,))
+    E, k = cfg.num_experts, cfg.num_active
+    ld = _rows("logits", logits, E)
+    T, dev = logits.shape[0], logits.device
+    b = None if bias is None else _array("bias", bias, logits, torch.float32, (E,))
     if out is None:
-        w = torch.empty(T, k, dtype=torch.float32, device=logits.device)
-        idx = torch.empty(T, k, dtype=torch.int32, device=logits.device)
-        n = torch.empty(E, dtype=torch.int32, device=logits.device) if counts else None
+        w = torch.empty((T, k), dtype=torch.float32, device=dev)
+        idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+        n = torch.empty((E,), dtype=torch.int32, device=dev) if counts else None
     else:
         w, idx, n = out
         _array("weights", w, logits, torch.float32, (T, k))
         _array("topk_idx", idx, logits, torch.int32, (T, k))
-        _array("counts", n, logits, torch.int32, (E,))
-    _call(logits, B.moe_route, cfg._c[logits.dtype], _ptr(logits), ld, T, _ptr(bias), _ptr(w), _ptr(idx), _ptr(n))
+        if n is not None:
+            _array("counts", n, logits, torch.int32, (E,))
+    _call(logits, B.moe_route, cfg._c[logits.dtype], logits.data_ptr(), ld, T, b, w.data_ptr(), idx.data_ptr(),
+          None if n is None else n.data_ptr())
     return w, idx, n
 
 
@@ -99,16 +97,28 @@ def route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, topk_idx: t
                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The gradient with respect to logits, given that of route's weights [T][k] fp32."""
     ld = _rows("logits", logits, cfg.num_experts)
-    T, k = logits.shape[0], cfg.num_active
-    _array("grad_weights", grad_weights, logits, torch.float32, (T, k))
-    _array("topk_idx", topk_idx, logits, torch.int32, (T, k))
+    T = logits.shape[0]
+    shape = (T, cfg.num_active)
+    g = _array("grad_weights", grad_weights, logits, torch.float32, shape)
+    idx = _array("topk_idx", topk_idx, logits, torch.int32, shape)
     if out is None:
-        out = torch.empty(T, cfg.num_experts, dtype=logits.dtype, device=logits.device)
-    elif out.dtype != logits.dtype or out.shape != logits.shape or out.device != logits.device:
-        raise ValueError("out has to be like logits")
-    _call(logits, B.moe_route_backward, cfg._c[logits.dtype], _ptr(grad_weights), _ptr(logits), ld, _ptr(topk_idx), T,
-          _ptr(out), _rows("out", out))
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        out_ld = cfg.num_experts
+    else:
+        if out.dtype != logits.dtype or out.shape != logits.shape or out.device != logits.device:
+            raise ValueError("out has to be like logits")
+        out_ld = _rows("out", out)
+    _call(logits, B.moe_route_backward, cfg._c[logits.dtype], g, logits.data_ptr(), ld, idx, T, out.data_ptr(), out_ld)
     return out
+
+
+def _code_bytes(rows: int, cols: int) -> int:
+    return rows * (cols // 2)
+
+
+def _scale_bytes(fmt: str, rows: int, cols: int) -> int:
+    tile_k = 4 * _BLOCK[fmt]
+    return (rows + 127) // 128 * ((cols + tile_k - 1) // tile_k) * 512
 
 
 class MxTensor:
@@ -118,12 +128,12 @@ class MxTensor:
 
     def __init__(self, fmt: str, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int, groups: int = 1,
                  scale_exp: int = 0):
-        if fmt not in B.MOE_MX:
+        if fmt not in _BLOCK:
             raise ValueError(f"unknown format {fmt!r}")
         if cols < 32 or cols % 32:
             raise ValueError(f"a row needs a positive multiple of 32 elements, got {cols}")
-        for name, t, need in (("codes", codes, groups * B.moe_mx_codes_bytes(rows, cols)),
-                              ("scales", scales, groups * B.moe_mx_scales_bytes(B.MOE_MX[fmt], rows, cols))):
+        for name, t, need in (("codes", codes, groups * _code_bytes(rows, cols)),
+                              ("scales", scales, groups * _scale_bytes(fmt, rows, cols))):
             if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() < need or t.device != codes.device:
                 raise ValueError(f"{name}: at least {need} contiguous bytes on one device are needed")
         self.format, self.codes, self.scales = fmt, codes, scales
@@ -145,22 +155,27 @@ def mx_quantize(x: torch.Tensor, fmt: str = "mxfp4", row_index: Optional[torch.T
     row_index[r], and is left as it was where that is no row of x. `values`, in x's type,
     receives what the codes stand for; `out`: an MxTensor to write into."""
     ld = _rows("x", x)
-    rows, cols = (x.shape[0] if row_index is None else row_index.numel()), x.shape[1]
-    _array("row_index", row_index, x, torch.int32)
-    if fmt not in B.MOE_MX:
+    x_rows, cols = x.shape
+    if fmt not in _BLOCK:
         raise ValueError(f"unknown format {fmt!r}")
-    if values is not None and (values.dtype != x.dtype or values.shape != (rows, cols) or values.device != x.device):
-        raise ValueError(f"values: {x.dtype} {(rows, cols)} on {x.device} is needed")
-    f = B.MOE_MX[fmt]
+    if row_index is None:
+        rows, index = x_rows, None
+    else:
+        rows, index = row_index.numel(), _array("row_index", row_index, x, torch.int32)
+    v = v_ld = 0
+    if values is not None:
+        if values.dtype != x.dtype or values.shape != (rows, cols) or values.device != x.device:
+            raise ValueError(f"values: {x.dtype} {(rows, cols)} on {x.device} is needed")
+        v, v_ld = values.data_ptr(), _rows("values", values)
     if out is None:
-        codes = torch.empty(rows, cols // 2, dtype=torch.uint8, device=x.device)
-        scales = torch.empty(B.moe_mx_scales_bytes(f, rows, cols), dtype=torch.uint8, device=x.device)
-        out = MxTensor(fmt, codes, scales, rows, cols, scale_exp=scale_exp)
+        codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=x.device)
+        scales = torch.empty((_scale_bytes(fmt, rows, cols),), dtype=torch.uint8, device=x.device)
+        out = MxTensor(fmt, codes, scales, rows, cols, 1, scale_exp)
     elif (out.format, out.rows, out.cols, out.groups, out.scale_exp) != (fmt, rows, cols, 1, scale_exp) or \
             out.codes.device != x.device:
         raise ValueError("out has another format, size, exponent or device")
-    _call(x, B.moe_mx_quantize, f, _ptr(x), _DTYPE[x.dtype], ld, x.shape[0], cols, _ptr(row_index), rows, scale_exp,
-          _ptr(out.codes), _ptr(out.scales), _ptr(values), 0 if values is None else _rows("values", values))
+    _call(x, B.moe_mx_quantize, B.MOE_MX[fmt], x.data_ptr(), _DTYPE[x.dtype], ld, x_rows, cols, index, rows, scale_exp,
+          out.codes.data_ptr(), out.scales.data_ptr(), v or None, v_ld)
     return out
 
 
@@ -171,8 +186,8 @@ def mx_dequantize(q: MxTensor, dtype: torch.dtype = torch.float32) -> torch.Tens
     if q.groups != 1:
         raise ValueError("one group at a time")
     out = torch.empty(q.rows, q.cols, dtype=dtype, device=q.codes.device)
-    _call(out, B.moe_mx_dequantize, B.MOE_MX[q.format], _ptr(q.codes), _ptr(q.scales), q.rows, q.cols, q.scale_exp,
-          _ptr(out), _DTYPE[dtype], q.cols)
+    _call(out, B.moe_mx_dequantize, B.MOE_MX[q.format], q.codes.data_ptr(), q.scales.data_ptr(), q.rows, q.cols,
+          q.scale_exp, out.data_ptr(), _DTYPE[dtype], q.cols)
     return out
 
 
@@ -193,22 +208,29 @@ def mx_gemm(a: MxTensor, w: MxTensor, group_start: Optional[torch.Tensor] = None
     if w.codes.device != like.device:
         raise ValueError("operands on different devices")
     G, n = w.groups, w.rows
-    for name, t in (("group_start", group_start), ("group_rows", group_rows)):
-        if t is not None:
-            _array(name, t, like, torch.int32)
-            if t.numel() < G:
-                raise ValueError(f"{name}: one entry for each of {G} groups is needed")
-    _array("bias", bias, like, torch.float32, (G, n))
-    _array("alpha", alpha, like, torch.float32, (G,))
-    _array("status", status, like, torch.int32, (1,))
+    start = rows = None
+    if group_start is not None:
+        start = _array("group_start", group_start, like, torch.int32)
+    if group_rows is not None:
+        rows = _array("group_rows", group_rows, like, torch.int32)
+    if (start is not None and group_start.numel() < G) or (rows is not None and group_rows.numel() < G):
+        raise ValueError(f"group_start and group_rows: one entry for each of {G} groups is needed")
+    b = None if bias is None else _array("bias", bias, like, torch.float32, (G, n))
+    al = None if alpha is None else _array("alpha", alpha, like, torch.float32, (G,))
+    st = None if status is None else _array("status", status, like, torch.int32, (1,))
+    if activation is None or activation == "none":
+        act = B.MOE_ACT_NONE
+    elif activation in B.MOE_ACT:
+        act = B.MOE_ACT[activation]
+    else:
+        raise ValueError(f"unknown activation {activation!r}")
     if out is None:
-        out = torch.empty(a.rows, n, dtype=dtype, device=like.device)
+        out = torch.empty((a.rows, n), dtype=dtype, device=like.device)
     elif out.device != like.device or out.shape[0] != a.rows:
         raise ValueError(f"out: {a.rows} rows on {like.device} are needed")
     ld = _rows("out", out, n)
-    act = B.MOE_ACT_NONE if activation in (None, "none") else B.MOE_ACT[activation]
     args = B.MoeMxGemm(B.MOE_MX[a.format], a.rows, n, a.cols, G, a.scale_exp + w.scale_exp, act, _DTYPE[out.dtype], ld,
-                       _ptr(a.codes), _ptr(a.scales), _ptr(w.codes), _ptr(w.scales), _ptr(group_start),
-                       _ptr(group_rows), _ptr(bias), _ptr(alpha), _ptr(out), _ptr(status))
+                       like.data_ptr(), a.scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(), start, rows, b, al,
+                       out.data_ptr(), st)
     _call(like, B.moe_mx_gemm, args)
     return out

@@ -31,6 +31,7 @@
 //
 // What bounds it: the instructions, about 450 a token for 256 experts in 8 groups.
 #include <algorithm>
+#include <type_traits>
 
 #include "route_common.cuh"
 #include "route_scores.cuh"
@@ -38,28 +39,14 @@
 namespace moe {
 namespace {
 
-// Threads of a forward block: more in the one-cluster form, where a warp should
-// have few tokens; 256 where the rows' buffers or the registers of 16 experts a lane ask for it.
-template <int RE, bool CLUSTER>
-constexpr int kForwardThreads = CLUSTER && RE <= 8 ? 512 : 256;
+constexpr int kThreads = 256;   // of the forward
+constexpr int kWarps = kThreads / 32;
+constexpr int kUndecided = 256;  // undecided tokens that a block puts by
 constexpr int kMaxCluster = 8;  // blocks that put their counts together without atomics
 constexpr int kBackThreads = 256;
 constexpr int kBackWarps = kBackThreads / 32;
 
 __device__ __forceinline__ double neg_inf() { return __longlong_as_double(0xfff0000000000000ll); }
-
-// (key, index) of the warp's highest key, the lower index between equal ones.
-__device__ __forceinline__ void warp_argmax(double &key, int &e) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        const double ok = __shfl_xor_sync(0xffffffffu, key, off);
-        const int oe = __shfl_xor_sync(0xffffffffu, e, off);
-        if (ok > key || (ok == key && oe < e)) {
-            key = ok;
-            e = oe;
-        }
-    }
-}
 
 __device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
@@ -73,88 +60,153 @@ __device__ __forceinline__ float logit(const XT *src, int e) {
     return l != l ? -INFINITY : l;
 }
 
-// Routes a token with keys in 64 bits, which `key` [E], in shared memory, takes.
-// Lane r returns choice r: its expert (-1: none) and its weight.
-template <typename XT>
-__device__ __noinline__ void route_exact(const XT *src, double *key, const RouteArgs &a, int lane, int &choice,
-                                         float &weight) {
-    float m = -INFINITY;
-    for (int e = lane; e < a.E; e += 32) m = fmaxf(m, logit(src, e));
+// What a lane needs to know of the groups, once for all tokens: `width` lanes (a power
+// of two) look at each group of experts, this one at those of group g from base on,
+// below `end`, `width` apart; every lane takes `steps` steps. bit[q]: the first lane
+// of expert lane + 32 q's group.
+template <int RE>
+struct Groups {
+    int width, g, steps, base, end;
+    uint32_t bit[RE];
+
+    __device__ __forceinline__ Groups(const RouteArgs &a, int lane) {
+        width = a.groups > 16 ? 1 : a.groups > 8 ? 2 : a.groups > 4 ? 4 : a.groups > 2 ? 8 : 16;
+        g = lane / width;
+        const int gs = a.E / a.groups;
+        steps = (gs + width - 1) / width;
+        base = g * gs + lane % width;
+        end = min(g + 1, a.groups) * gs;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    double z = 1.0;
-    if (!a.sigmoid) {
+        for (int q = 0; q < RE; ++q) bit[q] = 1u << min((lane + 32 * q) / gs, a.groups - 1) * width;
+    }
+
+    // Whether expert lane + 32 q's group has its bit in `lanes`.
+    __device__ __forceinline__ bool in(uint32_t lanes, int q) const {
+        return (lanes & bit[q]) != 0u;
+    }
+};
+
+__device__ __forceinline__ float warp_max(float v) {
+    return code_key(__reduce_max_sync(0xffffffffu, key_code(v)));
+}
+
+// The maximum of a token's logits (src: its row).
+template <typename XT>
+__device__ __forceinline__ float top_logit(const XT *src, int E, int lane) {
+    float m = -INFINITY;
+    for (int e = lane; e < E; e += 32) m = fmaxf(m, logit(src, e));
+    return warp_max(m);
+}
+
+// Step 1 of a token in 64 bits, by the whole block: an expert a thread, as the
+// exponentials' latency is what these tokens cost. row: what the keys are made of,
+// the logit, the sigmoid or exp(l - m); -inf for masked experts.
+template <typename XT, int RE>
+__device__ __forceinline__ void exact_scores(const XT *src, double *row, const RouteArgs &a, int lane) {
+    const bool by_logit = !a.bias && a.groups == 1;
+    const float m = a.sigmoid || by_logit ? 0.f : top_logit(src, a.E, lane);
+    for (int e = threadIdx.x; e < 32 * RE; e += blockDim.x) {
+        const float l = e < a.E ? logit(src, e) : -INFINITY;
+        double v = (double)l;
+        if (l != -INFINITY && !by_logit) {
+            const double x = exp(a.sigmoid ? -v : v - (double)m);
+            v = a.sigmoid ? 1.0 / (1.0 + x) : x;
+        }
+        row[e] = v;
+    }
+}
+
+// Step 2, by a warp. Lane l holds experts l + 32 q; lane r returns choice r: its
+// expert (-1: none) and its weight's bits.
+template <typename XT, int RE>
+__device__ __forceinline__ int2 route_exact(const XT *src, double *row, const RouteArgs &a, int lane) {
+    const bool by_logit = !a.bias && a.groups == 1;
+    const float m = a.sigmoid ? 0.f : top_logit(src, a.E, lane);
+    double key[RE], z = 1.0;
+#pragma unroll
+    for (int q = 0; q < RE; ++q) key[q] = row[lane + 32 * q];
+    if (!a.sigmoid && !(by_logit && a.renormalize)) {
         z = 0.0;
-        for (int e = lane; e < a.E; e += 32) {
-            const float l = logit(src, e);
-            if (l != -INFINITY) z += exp((double)l - (double)m);
+        for (int q = 0; q < RE; ++q) {
+            const double v = row[lane + 32 * q];
+            if (v != neg_inf()) z += by_logit ? exp(v - (double)m) : v;
         }
         z = warp_sum(z);
     }
-    auto score = [&](float l) {
-        if (l == -INFINITY) return 0.0;
-        return a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)m) / z;
-    };
-    for (int e = lane; e < a.E; e += 32) {
-        const float l = logit(src, e);
-        double v = neg_inf();
-        if (l != -INFINITY) {
-            if (a.bias) v = score(l) + (double)a.bias[e];
-            else v = a.groups > 1 ? score(l) : (double)l;
-            if (v != v) v = neg_inf();
+    if (!by_logit) {
+#pragma unroll
+        for (int q = 0; q < RE; ++q) {
+            if (!a.sigmoid && key[q] != neg_inf()) key[q] /= z;
+            if (a.bias && lane + 32 * q < a.E) key[q] += (double)a.bias[lane + 32 * q];
+            if (key[q] != key[q]) key[q] = neg_inf();
         }
-        key[e] = v;
     }
-    __syncwarp();
     if (a.groups > 1) {
-        const int gs = a.E / a.groups;
-        double mine = neg_inf();  // lane g: the score of group g
-        if (lane < a.groups) {
-            double t1 = neg_inf(), t2 = neg_inf();
-            for (int e = lane * gs; e < (lane + 1) * gs; ++e) {
-                const double v = key[e];
-                if (v > t1) {
-                    t2 = t1;
-                    t1 = v;
-                } else if (v > t2) {
-                    t2 = v;
-                }
-            }
-            mine = a.group_top == 2 && t2 != neg_inf() ? t1 + t2 : t1;
+        const Groups<RE> gr(a, lane);
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < RE; ++q) row[lane + 32 * q] = key[q];
+        __syncwarp();
+        double t1 = neg_inf(), t2 = neg_inf();
+        for (int e = gr.base; e < gr.end; e += gr.width) {
+            const double v = row[e];
+            t2 = v > t1 ? t1 : (v > t2 ? v : t2);
+            t1 = v > t1 ? v : t1;
         }
+        for (int off = 1; off < gr.width; off <<= 1) {
+            const double o1 = __shfl_xor_sync(0xffffffffu, t1, off), o2 = __shfl_xor_sync(0xffffffffu, t2, off);
+            const double low = o1 > t1 ? t1 : o1, second = o2 > t2 ? o2 : t2;
+            t1 = o1 > t1 ? o1 : t1;
+            t2 = low > second ? low : second;
+        }
+        const double mine = a.group_top == 2 && t2 != neg_inf() ? t1 + t2 : t1;
         int before = 0;
-        for (int g = 0; g < a.groups; ++g) {
-            const double o = __shfl_sync(0xffffffffu, mine, g);
-            if (o > mine || (o == mine && g < lane)) ++before;
+        for (int o = 0; o < a.groups; ++o) {
+            const double v = __shfl_sync(0xffffffffu, mine, o * gr.width);
+            before += v > mine || (v == mine && o < gr.g);
         }
-        const uint32_t in = __ballot_sync(0xffffffffu, lane < a.groups && before < a.top_groups);
-        __syncwarp();
-        for (int e = lane; e < a.E; e += 32)
-            if (!((in >> (e / gs)) & 1u)) key[e] = neg_inf();
-        __syncwarp();
+        const uint32_t lanes = __ballot_sync(0xffffffffu, gr.g < a.groups && before < a.top_groups);
+#pragma unroll
+        for (int q = 0; q < RE; ++q)
+            if (!gr.in(lanes, q)) key[q] = neg_inf();
     }
-    choice = -1;
+    // Order-preserving codes, as key_code's; those of -inf and below are no choice.
+    unsigned long long code[RE];
+    constexpr unsigned long long kNone = 0x0010000000000000ull;
+#pragma unroll
+    for (int q = 0; q < RE; ++q) {
+        const long long u = __double_as_longlong(key[q] + 0.0);
+        code[q] = static_cast<unsigned long long>(u) ^ (static_cast<unsigned long long>(u >> 63) | (1ull << 63));
+    }
+    int choice = -1;
+#pragma unroll 1
     for (int r = 0; r < a.k; ++r) {
-        double best = neg_inf();
-        int be = kRouteMaxExperts;
-        for (int e = lane; e < a.E; e += 32)
-            if (key[e] > best) {
-                best = key[e];
-                be = e;
-            }
-        warp_argmax(best, be);
-        if (best == neg_inf()) break;
-        if (lane == r) choice = be;
-        if (lane == (be & 31)) key[be] = neg_inf();
-        __syncwarp();
+        unsigned long long best = code[0];
+        int e = lane;
+#pragma unroll
+        for (int q = 1; q < RE; ++q) {
+            e = code[q] > best ? lane + 32 * q : e;
+            best = code[q] > best ? code[q] : best;
+        }
+        const uint32_t hi = static_cast<uint32_t>(best >> 32), lo = static_cast<uint32_t>(best);
+        const uint32_t top_hi = __reduce_max_sync(0xffffffffu, hi);
+        const uint32_t top_lo = __reduce_max_sync(0xffffffffu, hi == top_hi ? lo : 0u);
+        const uint32_t be = __reduce_min_sync(0xffffffffu, hi == top_hi && lo == top_lo ? static_cast<uint32_t>(e) : 0xffffu);
+        if ((static_cast<unsigned long long>(top_hi) << 32 | top_lo) < kNone) break;
+        if (lane == r) choice = static_cast<int>(be);
+#pragma unroll
+        for (int q = 0; q < RE; ++q) code[q] = be == static_cast<uint32_t>(lane + 32 * q) ? 0ull : code[q];
     }
-    double s = choice >= 0 ? score(logit(src, choice)) : 0.0;
+    double s = 0.0;
+    if (choice >= 0) {
+        const double l = (double)logit(src, choice);
+        s = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)m) / z;
+    }
     if (a.renormalize) {
         const double sum = warp_sum(s);
         s = sum > 0.0 ? s / sum : 0.0;
     }
-    weight = static_cast<float>(s * (double)a.scale);
-    __syncwarp();
+    return make_int2(choice, __float_as_int(static_cast<float>(s * (double)a.scale)));
 }
 
 __device__ __forceinline__ void cas32(uint32_t &x, uint32_t &y) {
@@ -177,132 +229,154 @@ __device__ __forceinline__ void sort32(uint32_t (&v)[RE]) {
                     if (i + j + k < RE && (i + j) / (2 * p) == (i + j + k) / (2 * p)) cas32(v[i + j], v[i + j + k]);
 }
 
+__device__ __forceinline__ uint32_t select(uint32_t which, uint32_t x, uint32_t y) {
+    uint32_t r;
+    asm("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\tselp.b32 %0, %1, %2, p;\n\t}" : "=r"(r) : "r"(x), "r"(y), "r"(which));
+    return r;
+}
+
+// What a token's keys are: its logits (no bias, no groups), or its scores with the biases, without and
+// with groups.
+enum { kByLogit = 0, kByScore = 1, kGrouped = 2 };
+
+// Where expert e's fp32 key lies in a warp's buffer: four places more every 32, so that the lanes that look
+// at groups of 32 experts read different banks.
+constexpr int kPad = 36;
+__device__ __forceinline__ int padded(int e) { return e + (e >> 5) * (kPad - 32); }
+
 // Two highest of two pairs (a1 >= a2, b1 >= b2).
 __device__ __forceinline__ void merge_top2(float &a1, float &a2, float b1, float b2) {
     a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
     a1 = fmaxf(a1, b1);
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-    return code_key(__reduce_max_sync(0xffffffffu, key_code(v)));
-}
-
-// Lanes (a power of two) that look at each group of experts.
-__device__ __forceinline__ int lanes_per_group(int groups) {
-    return groups > 16 ? 1 : groups > 8 ? 2 : groups > 4 ? 4 : groups > 2 ? 8 : 16;
-}
-
 // Routes a token on fp32 keys; false if they do not decide it. Lane l holds experts
-// l + 32 q: h[q] is the logit, -inf for experts that are not there or masked. `row`
-// is the warp's shared buffer, holding the logits; keys: a second one. bias: the lane's experts' biases; group_lane: in byte q the first lane
-// of the group of expert lane + 32 q.
-template <int RE>
-__device__ __forceinline__ bool route_fast(const float (&h)[RE], const float (&bias)[RE],
-                                           const uint32_t (&group_lane)[(RE + 3) / 4], const float *row, float *keys,
-                                           const RouteArgs &a, bool exact_codes, int lane, int &choice, float &weight) {
+// l + 32 q: h[q] is the logit, -inf for experts that are not there, -inf or NaN for masked ones;
+// bias: the experts' biases. `row` is the warp's shared buffer, holding the logits; keys: a
+// second one.
+template <int RE, int MODE, bool SIGMOID>
+__device__ __forceinline__ bool route_fast(float (&h)[RE], const float *bias, const Groups<RE> &gr,
+                                           const float *row, float *keys, const RouteArgs &a, bool exact_codes, int lane,
+                                           int &choice, float &weight) {
+    constexpr uint32_t kLow = 32 * RE - 1;     // the index bits of a code
+    constexpr uint32_t kNone = 0x00800000u;    // codes of finite keys are not below, those of -inf are
+    constexpr bool by_logit = MODE == kByLogit;
     choice = -1;
     weight = 0.f;
-    constexpr uint32_t kLow = 32 * RE - 1;  // the index bits of a code
-    const bool by_logit = !a.bias && a.groups == 1;
-    const bool need_all = !by_logit || (!a.sigmoid && !a.renormalize);  // every score, or those of the selection alone
     float m = 0.f, z = 1.f;
     float key[RE];
-    if (!a.sigmoid) {
+    if constexpr (!SIGMOID) {
+#pragma unroll
+        for (int q = 0; q < RE; ++q) h[q] = fmaxf(h[q], -INFINITY);  // a NaN is a masked logit
         m = h[0];
 #pragma unroll
         for (int q = 1; q < RE; ++q) m = fmaxf(m, h[q]);
         m = warp_max(m);
         if (m == -INFINITY) return true;  // nothing to select
-    }
-    if (need_all) {
-        float sum = 0.f;
+        if (!by_logit || !a.renormalize) {  // every score
+            float sum = 0.f;
 #pragma unroll
-        for (int q = 0; q < RE; ++q) {
-            key[q] = a.sigmoid ? __fdividef(1.f, 1.f + __expf(-h[q])) : expf(h[q] - m);
-            sum += key[q];
-        }
-        if (!a.sigmoid) {
+            for (int q = 0; q < RE; ++q) {
+                key[q] = expf(h[q] - m);
+                sum += key[q];
+            }
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
             z = 1.f / sum;
-        }
 #pragma unroll
-        for (int q = 0; q < RE; ++q) key[q] *= z;
+            for (int q = 0; q < RE; ++q) key[q] *= z;
+        }
+    } else if constexpr (!by_logit) {
+#pragma unroll
+        for (int q = 0; q < RE; ++q) key[q] = __fdividef(1.f, 1.f + __expf(-h[q]));
     }
     bool sure = true;
-    const float smax = a.sigmoid ? 1.f : z;  // no score is larger (a softmax's largest is exp(0) z)
-    if (by_logit) {
+    const float smax = SIGMOID ? 1.f : z;  // no score is larger (a softmax's largest is exp(0) z)
+    if constexpr (by_logit) {
 #pragma unroll
-        for (int q = 0; q < RE; ++q) key[q] = h[q];
+        for (int q = 0; q < RE; ++q) key[q] = fmaxf(h[q] + 0.f, -INFINITY);  // one zero for both signs, NaN masked
     } else {
+        // 0 h is NaN for a masked expert (-inf or NaN), and so is its key, and the key of a NaN bias; the
+        // maximum with -inf is -inf then.
 #pragma unroll
         for (int q = 0; q < RE; ++q) {
-            key[q] = h[q] == -INFINITY ? -INFINITY : (a.bias ? key[q] + bias[q] : key[q]);
-            if (key[q] != key[q]) key[q] = -INFINITY;
+            key[q] = fmaxf(fmaf(h[q], 0.f, key[q]) + (a.bias ? bias[lane + 32 * q] : 0.f), -INFINITY);
+            keys[lane + kPad * q] = key[q];
         }
-    }
-    if (!by_logit) {
-#pragma unroll
-        for (int q = 0; q < RE; ++q) keys[lane + 32 * q] = key[q];
         __syncwarp();
     }
-    if (a.groups > 1) {
-        const int gs = a.E / a.groups;
-        const int width = lanes_per_group(a.groups), g = lane / width;
+    if constexpr (MODE == kGrouped) {
         float t1 = -INFINITY, t2 = -INFINITY;
-        if (g < a.groups)
-            for (int i = lane % width; i < gs; i += width) {
-                const float v = keys[g * gs + i];
-                t2 = fmaxf(t2, fminf(t1, v));
-                t1 = fmaxf(t1, v);
-            }
-        for (int off = 1; off < width; off <<= 1)
-            merge_top2(t1, t2, __shfl_xor_sync(0xffffffffu, t1, off), __shfl_xor_sync(0xffffffffu, t2, off));
-        const float mine = t1 == -INFINITY ? -INFINITY : (a.group_top == 2 && t2 != -INFINITY ? t1 + t2 : t1);
-        int before = 0;
-        for (int o = 0; o < a.groups; ++o) {
-            const float v = __shfl_sync(0xffffffffu, mine, o * width);
-            if (v > mine || (v == mine && o < g)) ++before;
+#pragma unroll 4
+        for (int j = 0, e = gr.base; j < gr.steps; ++j, e += gr.width) {
+            const float v = e < gr.end ? keys[padded(e)] : -INFINITY;
+            t2 = fmaxf(t2, fminf(t1, v));
+            t1 = fmaxf(t1, v);
         }
-        const bool chosen = g < a.groups && before < a.top_groups;
+        __syncwarp();
+        for (int off = 1; off < gr.width; off <<= 1)
+            merge_top2(t1, t2, __shfl_xor_sync(0xffffffffu, t1, off), __shfl_xor_sync(0xffffffffu, t2, off));
+        const float mine = a.group_top == 2 && t2 != -INFINITY ? t1 + t2 : t1;
+        // Scores with the group's index in the lowest bits: the check below sees to those that this puts out
+        // of order.
+        const uint32_t rank = (key_code(mine) & ~31u) | (31u - gr.g);
+        int before = 0;
+#pragma unroll 4
+        for (int o = 0; o < a.groups; ++o) before += __shfl_sync(0xffffffffu, rank, o * gr.width) > rank;
+        const bool there = gr.g < a.groups, chosen = there && before < a.top_groups;
         const uint32_t lanes = __ballot_sync(0xffffffffu, chosen);
         if (a.top_groups < a.groups) {
-            // The lowest group inside against the highest one outside.
-            const float in = -warp_max(chosen ? -mine : -INFINITY), out = warp_max(!chosen && g < a.groups ? mine : -INFINITY);
-            if (out != -INFINITY && !(in - out > 0x1p-16f * fmaxf(smax, fmaxf(fabsf(in), fabsf(out))))) sure = false;
+            // The lowest group inside against the highest one outside: two scores each, and the codes' 5 bits.
+            const float in = -warp_max(chosen ? -mine : -INFINITY), out = warp_max(there && !chosen ? mine : -INFINITY);
+            if (out != -INFINITY && !(in - out > 0x1p-17f * smax + 0x1p-22f * (fabsf(in) + fabsf(out)))) sure = false;
         }
 #pragma unroll
         for (int q = 0; q < RE; ++q)
-            if (!((lanes >> (group_lane[q / 4] >> (8 * (q % 4)) & 31u)) & 1u)) key[q] = -INFINITY;
+            if (!gr.in(lanes, q)) key[q] = -INFINITY;
     }
     uint32_t code[RE];
+    const uint32_t low = 31u & ~static_cast<uint32_t>(lane);
 #pragma unroll
-    for (int q = 0; q < RE; ++q)
-        code[q] = key[q] == -INFINITY ? 0u : (key_code(key[q]) & ~kLow) | (kLow - (lane + 32 * q));
-    sort32<RE>(code);
-    for (int r = 0; r < a.k; ++r) {
-        const uint32_t top = __reduce_max_sync(0xffffffffu, code[0]);
-        if (code[0] == top) {
-#pragma unroll
-            for (int q = 0; q + 1 < RE; ++q) code[q] = code[q + 1];
-            code[RE - 1] = 0u;
-        }
-        if (lane == r && top != 0u) choice = static_cast<int>(kLow - (top & kLow));
+    for (int q = 0; q < RE; ++q) {
+        const uint32_t u = __float_as_uint(key[q]);
+        const uint32_t c = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+        code[q] = (c & ~kLow) | (low + 32u * (RE - 1 - q));  // the complement of the expert's index below
     }
+    sort32<RE>(code);
+    // A lane that holds more than kDepth of up to 8 choices (0.1% of the tokens, 256 experts) is not followed
+    // further: each round costs a select for every key that can come up.
+    constexpr int kDepth = RE < 4 ? RE : 4;
+    auto rounds = [&](auto depth) {
+        constexpr int D = decltype(depth)::value;
+#pragma unroll 1
+        for (int r = 0; r < a.k; ++r) {
+            const uint32_t top = __reduce_max_sync(0xffffffffu, code[0]);
+            const uint32_t mine = code[0] == top;
+#pragma unroll
+            for (int q = 0; q < D; ++q) code[q] = select(mine, q + 1 < D ? code[q + 1] : 0u, code[q]);
+            if (lane == r) choice = static_cast<int>(top);
+        }
+    };
+    if (a.k <= 8) rounds(std::integral_constant<int, kDepth>{});
+    else rounds(std::integral_constant<int, RE>{});
+    choice = lane < a.k && static_cast<uint32_t>(choice) >= kNone ? static_cast<int>(kLow - (choice & kLow)) : -1;
+    if (RE > kDepth && a.k <= 8 && __any_sync(0xffffffffu, code[0] == 0u && code[RE > kDepth ? kDepth : 0] >= kNone)) sure = false;
     const uint32_t left = __reduce_max_sync(0xffffffffu, code[0]);  // the first one left out
-    if (by_logit) {
+    float l = row[max(choice, 0)];
+    l = choice >= 0 ? l : -INFINITY;
+    if constexpr (by_logit) {
         // Equal logits are in the order of their indices; where fp32 logits have equal codes at the
         // border, the ones left out may be higher.
-        const float v = choice >= 0 ? row[choice] : -INFINITY;
-        const float next = __shfl_down_sync(0xffffffffu, v, 1);
-        bool fine = lane >= a.k - 1 || v >= next;
-        if (!exact_codes && lane == a.k - 1 && choice >= 0 && left != 0u)
-            fine = (key_code(v) & ~kLow) > (left & ~kLow);
-        sure = __all_sync(0xffffffffu, fine);
+        const float next = __shfl_down_sync(0xffffffffu, l, 1);
+        bool fine = lane >= a.k - 1 || l >= next;
+        if (!exact_codes && lane == a.k - 1 && choice >= 0 && left >= kNone)
+            fine = (key_code(l) & ~kLow) > (left & ~kLow);
+        if (!__all_sync(0xffffffffu, fine)) sure = false;
     } else {
-        const float v = choice >= 0 ? keys[choice] : -INFINITY;
+        float v = keys[padded(max(choice, 0))];
+        v = choice >= 0 ? v : -INFINITY;
         float next = __shfl_down_sync(0xffffffffu, v, 1);
-        if (lane == a.k - 1) next = left != 0u ? code_key(left | kLow) : -INFINITY;
+        if (lane == a.k - 1) next = left >= kNone ? code_key(left | kLow) : -INFINITY;
         const float error = a.bias ? 0x1p-18f * smax + 0x1p-23f * fabsf(v) : 0x1p-18f * v;
         const bool fine = lane >= a.k || next == -INFINITY || v - next > error;
         // Scores without a bias that are too small for the bounds are left to 64 bits.
@@ -311,17 +385,15 @@ __device__ __forceinline__ bool route_fast(const float (&h)[RE], const float (&b
     }
     if (!sure) return false;
     // The scores of the selection, from its logits.
-    const float l = choice >= 0 ? row[choice] : -INFINITY;
-    float s;
-    if (a.sigmoid) s = choice >= 0 ? 1.f / (1.f + expf(-l)) : 0.f;
-    else s = choice >= 0 ? expf(l - m) * z : 0.f;
+    float s = 0.f;
+    s = SIGMOID ? __fdividef(1.f, 1.f + expf(-l)) : expf(l - m) * z;
+    s = choice >= 0 ? s : 0.f;
     if (a.renormalize) {
         float sum = s;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        for (int off = 1; off < a.k; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         // Scores so small that fp32 loses them are left to 64 bits.
-        if (!(sum > 0x1p-80f)) return sum == 0.f && __all_sync(0xffffffffu, choice < 0);
-        s = s / sum;
+        if (!__all_sync(0xffffffffu, lane >= a.k || sum > 0x1p-80f)) return __all_sync(0xffffffffu, choice < 0);
+        s = __fdividef(s, sum);
     }
     weight = s * a.scale;
     return true;
@@ -333,52 +405,81 @@ __device__ __forceinline__ int ld_shared_cluster(uint32_t addr) {
     return v;
 }
 
-// CLUSTER: the whole grid is one cluster, whose blocks add their counts up among
+// cluster: the whole grid is one cluster, whose blocks add their counts up among
 // themselves; otherwise they are added to `counts` (zeroed before) by atomics.
-template <typename XT, int RE, bool CLUSTER>
-__global__ void __launch_bounds__(kForwardThreads<RE, CLUSTER>, CLUSTER ? 1 : RE > 8 ? 2 : 3)
-    route_kernel(const RouteArgs a) {
-    constexpr int kThreads = kForwardThreads<RE, CLUSTER>, kWarps = kThreads / 32;
+template <typename XT, int RE, int MODE, bool SIGMOID>
+__global__ void __launch_bounds__(kThreads, RE > 8 ? 2 : 3) route_kernel(const __grid_constant__ RouteArgs a, bool cluster) {
     __shared__ int32_t hist[kRouteMaxExperts];
-    __shared__ __align__(8) float rows[kWarps][2][32 * RE];  // logits and keys, or a row of 64-bit keys
+    __shared__ __align__(8) float rows[kWarps][(32 + kPad) * RE];  // logits and keys, or a row of 64-bit keys
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (a.counts) {
-        for (int e = threadIdx.x; e < a.E; e += kThreads) hist[e] = 0;
-        __syncthreads();
-    }
-    float *row = rows[warp][0], *keys = rows[warp][1];
-    float bias[RE];
-#pragma unroll
-    for (int q = 0; q < RE; ++q) bias[q] = a.bias && lane + 32 * q < a.E ? a.bias[lane + 32 * q] : 0.f;
-    uint32_t group_lane[(RE + 3) / 4] = {};
-#pragma unroll
-    for (int q = 0; q < RE; ++q)
-        group_lane[q / 4] |= static_cast<uint32_t>(min((lane + 32 * q) / (a.E / a.groups), a.groups - 1) *
-                                                   lanes_per_group(a.groups)) << (8 * (q % 4));
-    for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.T; t += (int64_t)gridDim.x * kWarps) {
+    for (int e = threadIdx.x; e < kRouteMaxExperts; e += kThreads) hist[e] = 0;
+    float *row = rows[warp], *keys = rows[warp] + 32 * RE;
+    __shared__ float bias[32 * RE];
+    __shared__ int undecided[kUndecided], n_undecided;  // tokens of this block left to route_exact
+    for (int e = threadIdx.x; e < 32 * RE; e += kThreads) bias[e] = a.bias && e < a.E ? a.bias[e] : 0.f;
+    if (threadIdx.x == 0) n_undecided = 0;
+    __syncthreads();
+    const Groups<RE> gr(a, lane);
+    auto token = [&](int i) { return blockIdx.x + (int64_t)gridDim.x * i; };
+    float ahead[RE];
+    auto load = [&](int64_t t) {
+        if (t >= a.T) return;
         const XT *src = static_cast<const XT *>(a.logits) + t * a.ld;
-        float h[RE];
+        if (a.E == 32 * RE) {
 #pragma unroll
-        for (int q = 0; q < RE; ++q) h[q] = lane + 32 * q < a.E ? to_f32(src[lane + 32 * q]) : -INFINITY;
+            for (int q = 0; q < RE; ++q) ahead[q] = to_f32(src[lane + 32 * q]);
+        } else {
 #pragma unroll
-        for (int q = 0; q < RE; ++q) {
-            if (h[q] != h[q]) h[q] = -INFINITY;
-            row[lane + 32 * q] = h[q];
+            for (int q = 0; q < RE; ++q) ahead[q] = lane + 32 * q < a.E ? to_f32(src[lane + 32 * q]) : -INFINITY;
         }
-        __syncwarp();
-        int choice;
-        float weight;
-        if (!route_fast<RE>(h, bias, group_lane, row, keys, a, sizeof(XT) == 2, lane, choice, weight))
-            route_exact<XT>(src, reinterpret_cast<double *>(row), a, lane, choice, weight);
+    };
+    auto write = [&](int64_t t, int choice, float weight) {
         if (lane < a.k) {
             a.idx[t * a.k + lane] = choice;
             a.weights[t * a.k + lane] = weight;
             if (a.counts && choice >= 0) atomicAdd(&hist[choice], 1);
         }
-        __syncwarp();
-    }
+    };
+    // Block b has tokens b, b + blocks, ..., its warps in turn. Undecided ones are put by and routed, by all
+    // warps together, when the block has no others left (or no room for more).
+    int i = warp;
+    load(token(i));
+    do {
+        while (token(i) < a.T && *reinterpret_cast<volatile int *>(&n_undecided) <= kUndecided - kWarps) {
+            float h[RE];
+#pragma unroll
+            for (int q = 0; q < RE; ++q) row[lane + 32 * q] = h[q] = ahead[q];
+            const int next = i + kWarps;
+            load(token(next));  // the next token's logits, while this one is routed
+            __syncwarp();
+            int choice;
+            float weight;
+            if (route_fast<RE, MODE, SIGMOID>(h, bias, gr, row, keys, a, sizeof(XT) == 2, lane, choice, weight))
+                write(token(i), choice, weight);
+            else if (lane == 0)
+                undecided[atomicAdd(&n_undecided, 1)] = i;
+            i = next;
+            __syncwarp();
+        }
+        __syncthreads();
+        const int n = n_undecided;
+        for (int j0 = 0; j0 < n; j0 += kWarps) {
+            for (int j = j0; j < min(n, j0 + kWarps); ++j)
+                exact_scores<XT, RE>(static_cast<const XT *>(a.logits) + token(undecided[j]) * a.ld,
+                                     reinterpret_cast<double *>(rows[j - j0]), a, lane);
+            __syncthreads();
+            if (j0 + warp < n) {
+                const int64_t t = token(undecided[j0 + warp]);
+                const int2 r = route_exact<XT, RE>(static_cast<const XT *>(a.logits) + t * a.ld,
+                                                   reinterpret_cast<double *>(row), a, lane);
+                write(t, r.x, __int_as_float(r.y));
+            }
+            __syncthreads();
+        }
+        if (threadIdx.x == 0) n_undecided = 0;
+    } while (__syncthreads_or(token(i) < a.T));
     if (!a.counts) return;
-    if constexpr (CLUSTER) {
+    if (cluster) {
         cluster_sync_all();
         for (int e = blockIdx.x + gridDim.x * threadIdx.x; e < a.E; e += gridDim.x * kThreads) {
             int n = 0;
@@ -480,41 +581,51 @@ __global__ void __launch_bounds__(kBackThreads) route_backward_kernel(const Rout
     }
 }
 
-template <typename XT, int RE>
+template <typename XT, int RE, int MODE, bool SIGMOID>
 cudaError_t launch_forward(const RouteArgs &a, int num_sms, cudaStream_t s) {
+    const int64_t blocks = ((int64_t)a.T + kWarps - 1) / kWarps;
     // Up to four tokens a warp of one cluster: no zeroing of the counts before (2 us of host time and a
     // launch less; 128 tokens: 4 against 6 us on the device).
-    constexpr int kBig = kForwardThreads<RE, true>, kSmall = kForwardThreads<RE, false>;
-    if (a.counts && a.T <= 4 * kMaxCluster * (kBig / 32)) {
-        const int blocks = (a.T + kBig / 32 - 1) / (kBig / 32);
-        int n = 1;
+    const bool cluster = a.counts && blocks <= 4 * kMaxCluster;
+    int n = 1;
+    if (cluster) {
         while (n < kMaxCluster && n < blocks) n *= 2;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(n, 1, 1);
-        cfg.blockDim = dim3(kBig, 1, 1);
-        cfg.stream = s;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = n;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, route_kernel<XT, RE, true>, a);
+    } else {
+        if (a.counts) {
+            const cudaError_t e = cudaMemsetAsync(a.counts, 0, sizeof(int32_t) * a.E, s);
+            if (e != cudaSuccess) return e;
+        }
+        n = static_cast<int>(std::min<int64_t>(blocks, (int64_t)num_sms * (RE > 8 ? 2 : 3)));
     }
-    if (a.counts) {
-        const cudaError_t e = cudaMemsetAsync(a.counts, 0, sizeof(int32_t) * a.E, s);
-        if (e != cudaSuccess) return e;
-    }
-    const int64_t blocks = ((int64_t)a.T + kSmall / 32 - 1) / (kSmall / 32);
-    const int grid = static_cast<int>(std::min<int64_t>(blocks, (int64_t)num_sms * (RE > 8 ? 2 : 3)));
-    route_kernel<XT, RE, false><<<grid, kSmall, 0, s>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = n;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, route_kernel<XT, RE, MODE, SIGMOID>, a, cluster);
+}
+
+template <typename XT, int RE>
+cudaError_t launch_mode(const RouteArgs &a, int num_sms, cudaStream_t s) {
+    if (a.groups > 1)
+        return a.sigmoid ? launch_forward<XT, RE, kGrouped, true>(a, num_sms, s)
+                         : launch_forward<XT, RE, kGrouped, false>(a, num_sms, s);
+    if (a.bias)
+        return a.sigmoid ? launch_forward<XT, RE, kByScore, true>(a, num_sms, s)
+                         : launch_forward<XT, RE, kByScore, false>(a, num_sms, s);
+    return a.sigmoid ? launch_forward<XT, RE, kByLogit, true>(a, num_sms, s)
+                     : launch_forward<XT, RE, kByLogit, false>(a, num_sms, s);
 }
 
 template <typename XT, int RE>
 cudaError_t launch_both(const RouteArgs *f, const RouteBackwardArgs *b, int num_sms, cudaStream_t s) {
-    if (f) return launch_forward<XT, RE>(*f, num_sms, s);
+    if (f) return launch_mode<XT, RE>(*f, num_sms, s);
     const int grid =
         static_cast<int>(std::min<int64_t>(((int64_t)b->T + kBackWarps - 1) / kBackWarps, (int64_t)num_sms * 8));
     route_backward_kernel<XT, RE><<<grid, kBackThreads, 0, s>>>(*b);
@@ -524,7 +635,6 @@ cudaError_t launch_both(const RouteArgs *f, const RouteBackwardArgs *b, int num_
 template <typename XT>
 cudaError_t launch_any(const RouteArgs *f, const RouteBackwardArgs *b, int num_sms, cudaStream_t s) {
     const int E = f ? f->E : b->E;
-    if (E <= 32) return launch_both<XT, 1>(f, b, num_sms, s);
     if (E <= 64) return launch_both<XT, 2>(f, b, num_sms, s);
     if (E <= 128) return launch_both<XT, 4>(f, b, num_sms, s);
     if (E <= 256) return launch_both<XT, 8>(f, b, num_sms, s);

@@ -496,59 +496,63 @@ __global__ void __launch_bounds__(kThreads, RE > 8 ? 2 : 3) route_kernel(const _
 
 // The gradient of a token's weights with respect to its logits. Lane r holds
 // choice r; the row is put together in shared memory, so that an expert chosen
-// twice adds up (in the order of the choices).
-template <typename XT, int RE>
-__global__ void __launch_bounds__(kBackThreads) route_backward_kernel(const RouteBackwardArgs a) {
-    __shared__ float rows[kBackWarps][32 * RE];
+// twice adds up (in the order of the choices). Lane l writes (DENSE: also reads)
+// experts 4 l .. 4 l + 3 of every 128 in one access where the rows allow it.
+//
+// Bound by HBM where T E is large: the row is written once and read only where every
+// logit has a gradient (the softmax that is not renormalised).
+template <typename XT, int N>
+struct alignas(N * sizeof(XT)) Pack {
+    XT v[N];
+};
+
+template <typename XT, int RE, bool DENSE, bool VEC>
+__global__ void __launch_bounds__(kBackThreads) route_backward_kernel(const __grid_constant__ RouteBackwardArgs a) {
+    __shared__ __align__(16) float rows[kBackWarps][32 * RE];
+    constexpr int V = VEC ? (RE < 4 ? RE : 4) : 1, NV = RE / V;  // elements of an access, accesses
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float *buf = rows[warp];
-    const bool dense = !a.sigmoid && !a.renormalize;
-    for (int64_t t = (int64_t)blockIdx.x * kBackWarps + warp; t < a.T; t += (int64_t)gridDim.x * kBackWarps) {
+    auto at = [&](int i) { return (i * 32 + lane) * V; };  // the first element of access i
+    auto sum = [](float v) {
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+        return v;
+    };
+    const int64_t stride = (int64_t)gridDim.x * kBackWarps;
+#pragma unroll
+    for (int q = 0; q < RE; ++q) buf[lane + 32 * q] = 0.f;
+    for (int64_t t = (int64_t)blockIdx.x * kBackWarps + warp; t < a.T; t += stride) {
         const XT *row = static_cast<const XT *>(a.logits) + t * a.ld;
         int e = lane < a.k ? a.idx[t * a.k + lane] : -1;
         if (e >= a.E) e = -1;
-        const float g = e >= 0 ? a.grad_weights[t * a.k + lane] * a.scale : 0.f;
+        e = max(e, -1);
+        float g = lane < a.k ? a.grad_weights[t * a.k + lane] * a.scale : 0.f;
+        g = e >= 0 ? g : 0.f;
+        Pack<XT, V> raw[NV];
+        if constexpr (DENSE) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (at(i) < a.E) raw[i] = *reinterpret_cast<const Pack<XT, V> *>(row + at(i));
+        }
         float l = e >= 0 ? to_f32(row[e]) : -INFINITY;
-        float p[RE], m = l;
-        if (dense) {
-#pragma unroll
-            for (int q = 0; q < RE; ++q) {
-                p[q] = lane + 32 * q < a.E ? to_f32(row[lane + 32 * q]) : -INFINITY;
-                if (p[q] != p[q]) p[q] = -INFINITY;
-                m = fmaxf(m, p[q]);
-            }
-        }
-        if (l != l) l = -INFINITY;
-        float d, mean = 0.f;
-        auto sum = [](float v) {
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-            return v;
-        };
-        if (!a.sigmoid) {
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-        }
+        l = fmaxf(l, -INFINITY);  // a NaN is a masked logit
         const bool live = l != -INFINITY;
-        if (a.sigmoid) {
-            const float en = expf(-fabsf(l)), s = live ? (l >= 0.f ? 1.f : en) / (1.f + en) : 0.f;
-            const float ds = live ? (l >= 0.f ? en : 1.f) / (1.f + en) : 0.f;  // 1 - s
-            if (a.renormalize) {
-                const float total = sum(s);
-                const float w = total > 0.f ? s / total : 0.f;
-                d = w * (g - sum(g * w)) * ds;
-            } else {
-                d = g * s * ds;
-            }
-        } else if (a.renormalize) {
-            const float x = live ? expf(l - m) : 0.f, total = sum(x);
-            const float w = total > 0.f ? x / total : 0.f;
-            d = w * (g - sum(g * w));
-        } else {
+        float d, mean = 0.f, p[RE];
+        if constexpr (DENSE) {
+            float m = l;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    p[i * V + j] = at(i) < a.E ? fmaxf(to_f32(raw[i].v[j]), -INFINITY) : -INFINITY;
+                    m = fmaxf(m, p[i * V + j]);
+                }
+            m = warp_max(m);
+            if (m == -INFINITY) m = 0.f;  // no logit at all: every probability is 0
             float z = 0.f;
 #pragma unroll
             for (int q = 0; q < RE; ++q) {
-                p[q] = p[q] == -INFINITY ? 0.f : expf(p[q] - m);
+                p[q] = expf(p[q] - m);
                 z += p[q];
             }
             z = sum(z);
@@ -557,26 +561,46 @@ __global__ void __launch_bounds__(kBackThreads) route_backward_kernel(const Rout
             for (int q = 0; q < RE; ++q) p[q] *= inv;
             mean = sum(live ? g * expf(l - m) * inv : 0.f);
             d = g;
+        } else if (a.sigmoid) {
+            const float en = expf(-fabsf(l)), r = __fdividef(1.f, 1.f + en);
+            const float s = live ? (l >= 0.f ? r : en * r) : 0.f, ds = live ? (l >= 0.f ? en * r : r) : 0.f;  // s, 1 - s
+            d = g * s * ds;
+            if (a.renormalize) {
+                const float total = sum(s), w = total > 0.f ? s / total : 0.f;
+                d = w * (g - sum(g * w)) * ds;
+            }
+        } else {  // the softmax over the selection alone
+            const float m = warp_max(l), x = live ? expf(l - m) : 0.f, total = sum(x);
+            const float w = total > 0.f ? x / total : 0.f;
+            d = w * (g - sum(g * w));
         }
-#pragma unroll
-        for (int q = 0; q < RE; ++q) buf[lane + 32 * q] = 0.f;
-        __syncwarp();
         // The first lane of those with the same expert adds their terms up.
         const uint32_t same = __match_any_sync(0xffffffffu, e);
-        float total = 0.f;
-        for (int r = 0; r < a.k; ++r) {
-            const float o = __shfl_sync(0xffffffffu, d, r);
-            if ((same >> r) & 1u) total += o;
+        const uint32_t first = __ffs(same) - 1;
+        float total = d;
+        if (__any_sync(0xffffffffu, e >= 0 && (same & (same - 1)))) {
+            total = 0.f;
+            for (int r = 0; r < a.k; ++r) {
+                const float o = __shfl_sync(0xffffffffu, d, r);
+                if ((same >> r) & 1u) total += o;
+            }
         }
-        if (e >= 0 && lane == __ffs(same) - 1) buf[e] = total;
+        const bool put = e >= 0 && lane == static_cast<int>(first);
+        if (put) buf[e] = total;
         __syncwarp();
         XT *out = static_cast<XT *>(a.grad_logits) + t * a.grad_ld;
 #pragma unroll
-        for (int q = 0; q < RE; ++q) {
-            const int c = lane + 32 * q;
-            const float v = buf[c];
-            if (c < a.E) out[c] = from_f32<XT>(dense ? p[q] * (v - mean) : v);
+        for (int i = 0; i < NV; ++i) {
+            Pack<XT, V> o;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float v = buf[at(i) + j];
+                o.v[j] = from_f32<XT>(DENSE ? p[i * V + j] * (v - mean) : v);
+            }
+            if (at(i) < a.E) *reinterpret_cast<Pack<XT, V> *>(out + at(i)) = o;
         }
+        __syncwarp();
+        if (put) buf[e] = 0.f;  // the buffer is zero again for the next token
         __syncwarp();
     }
 }
@@ -626,9 +650,21 @@ cudaError_t launch_mode(const RouteArgs &a, int num_sms, cudaStream_t s) {
 template <typename XT, int RE>
 cudaError_t launch_both(const RouteArgs *f, const RouteBackwardArgs *b, int num_sms, cudaStream_t s) {
     if (f) return launch_mode<XT, RE>(*f, num_sms, s);
+    constexpr int V = RE < 4 ? RE : 4;
+    auto rows_of = [&](const void *p, int64_t ld) {
+        return reinterpret_cast<uintptr_t>(p) % (V * sizeof(XT)) == 0 && ld % V == 0;
+    };
+    const bool dense = !b->sigmoid && !b->renormalize;
+    const bool vec = b->E % V == 0 && rows_of(b->grad_logits, b->grad_ld) && (!dense || rows_of(b->logits, b->ld));
     const int grid =
         static_cast<int>(std::min<int64_t>(((int64_t)b->T + kBackWarps - 1) / kBackWarps, (int64_t)num_sms * 8));
-    route_backward_kernel<XT, RE><<<grid, kBackThreads, 0, s>>>(*b);
+    if (dense) {
+        if (vec) route_backward_kernel<XT, RE, true, true><<<grid, kBackThreads, 0, s>>>(*b);
+        else route_backward_kernel<XT, RE, true, false><<<grid, kBackThreads, 0, s>>>(*b);
+    } else {
+        if (vec) route_backward_kernel<XT, RE, false, true><<<grid, kBackThreads, 0, s>>>(*b);
+        else route_backward_kernel<XT, RE, false, false><<<grid, kBackThreads, 0, s>>>(*b);
+    }
     return cudaGetLastError();
 }
 

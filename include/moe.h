@@ -426,6 +426,18 @@ MOE_API int moe_route(const moe_route_config_t *cfg, const void *logits, int64_t
 MOE_API int moe_route_backward(const moe_route_config_t *cfg, const float *grad_weights, const void *logits, int64_t ld,
                                const int32_t *topk_idx, int32_t T, void *grad_logits, int64_t grad_ld, void *stream);
 
+/* From now on the layer's forwards (and moe_ep_dispatch) route as cfg says: the
+ * router's logits stay as they are, moe_route turns them into topk_idx and gates
+ * (one launch more), with weights->sel_bias as its bias where the layer has
+ * use_selection_bias (added to the scores, then). Choices that are left over
+ * (moe_route's -1) take the lowest free experts, with gate 0. The statistics P_i and
+ * l_z stay those of softmax(h); the others follow the selection and the gates. cfg
+ * is copied; NULL returns to the router's own selection. Not to be called between a
+ * forward and the statistics of it.
+ * Errors: INVALID_ARG (as moe_route; num_experts or num_active other than the
+ * layer's, dtype not FP32), UNSUPPORTED (NOISY layers). */
+MOE_API int moe_set_routing(moe_layer_t *layer, const moe_route_config_t *cfg);
+
 /* ------------------------------------------------------------------------
  * Microscaled 4-bit floating point: rows of E2M1 codes (magnitudes 0, 0.5, 1,
  * 1.5, 2, 3, 4, 6) with one scale per block of neighbouring elements.
@@ -499,6 +511,23 @@ typedef struct {
 } moe_mx_gemm_t;
 MOE_API int moe_mx_gemm(const moe_mx_gemm_t *args, void *stream);
 
+/* 4-bit experts of a bf16 layer with ep_size 1 (shared experts included): quantises
+ * w1 and w2 once, enqueued on `stream`, into `buffer` (device, caller-owned, >=
+ * moe_experts_mx_bytes(layer, format) bytes, 256-byte aligned, valid until it is
+ * replaced or the layer destroyed). Later forwards quantise the tokens' rows and,
+ * between the products, the bf16 hidden activations, and run both expert layers as
+ * moe_mx_gemm does; routing, capacity, combine, credit and statistics are the
+ * same. The experts' weights are as they were when this call ran; w1 and w2 are not
+ * read by forwards until it is undone. w1_exp and w2_exp: moe_mx_quantize's scale_exp
+ * of the two stacks (0 for MXFP4; NVFP4 wants about log2 of the weights' size).
+ * moe_workspace_bytes changes with this call: ask again. buffer = NULL returns to the
+ * bf16 experts. Call it between forwards: the statistics of an earlier forward are no
+ * longer to be had. Errors: INVALID_ARG, UNSUPPORTED (fp32 layers, ep_size > 1),
+ * WORKSPACE, CUDA. moe_experts_mx_bytes is 0 for fp32 layers, NULL and unknown formats. */
+MOE_API size_t moe_experts_mx_bytes(const moe_layer_t *layer, int32_t format);
+MOE_API int moe_prepare_experts_mx(moe_layer_t *layer, int32_t format, int32_t w1_exp, int32_t w2_exp, void *buffer,
+                                   size_t bytes, void *stream);
+
 /* Self-check of the bounded waits the tcgen05 kernels rely on (no counterpart
  * on the pages): one GPU thread waits on an mbarrier that nothing arrives on;
  * after the wait limit (2 s) it records the timeout and returns, as every role
@@ -510,7 +539,7 @@ MOE_API int moe_selftest_bounded_wait(void *stream);
 
 /* Self-check of the bounded waits inside the real expert GEMM (no counterpart on
  * the pages): one moe_forward of this layer over x [T][d] (GREEDY top-k, bf16,
- * ep_size 1, d >= 192) with workspace and y as for moe_forward, in which the
+ * ep_size 1, d >= 192, bf16 experts) with workspace and y as for moe_forward, in which the
  * expert-GEMM launch's leader CTAs announce the bytes of their third pipeline
  * stage but load none of them, and every wait of that launch gives up after
  * 20 ms. The MMA role's wait runs out, the kernel's roles stop (those waiting

@@ -31,7 +31,8 @@ EXPORTS = ("moe_config_default", "moe_layer_create", "moe_workspace_bytes", "moe
            "moe_selftest_router_timeout", "moe_router_planes_bytes", "moe_prepare_router",
            "moe_ep_dispatch", "moe_ep_layout", "moe_ep_experts_workspace_bytes", "moe_ep_experts", "moe_ep_combine", "moe_device_status", "moe_set_timing_events", "moe_launch_count", "moe_destroy", "moe_status_string",
            "moe_last_error", "moe_route_config_default", "moe_route", "moe_route_backward", "moe_mx_codes_bytes",
-           "moe_mx_scales_bytes", "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_gemm")
+           "moe_mx_scales_bytes", "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_gemm", "moe_set_routing",
+           "moe_experts_mx_bytes", "moe_prepare_experts_mx")
 
 
 class MoeConfig(ctypes.Structure):
@@ -165,6 +166,12 @@ def lib() -> ctypes.CDLL:
         L.moe_mx_dequantize.argtypes = [i32, vp, vp, i32, i32, i32, vp, i32, i64, vp]
         L.moe_mx_gemm.restype = ctypes.c_int
         L.moe_mx_gemm.argtypes = [ctypes.POINTER(MoeMxGemm), vp]
+        L.moe_set_routing.restype = ctypes.c_int
+        L.moe_set_routing.argtypes = [vp, ctypes.POINTER(MoeRouteConfig)]
+        L.moe_experts_mx_bytes.restype = sz
+        L.moe_experts_mx_bytes.argtypes = [vp, i32]
+        L.moe_prepare_experts_mx.restype = ctypes.c_int
+        L.moe_prepare_experts_mx.argtypes = [vp, i32, i32, i32, vp, sz, vp]
         _lib = L
     return _lib
 
@@ -323,6 +330,20 @@ def moe_mx_gemm(args: MoeMxGemm, stream: int) -> int:
     return _check(lib().moe_mx_gemm(ctypes.byref(args), stream), "moe_mx_gemm")
 
 
+def moe_set_routing(layer: int, cfg: Optional[MoeRouteConfig]) -> int:
+    return _check(lib().moe_set_routing(layer, ctypes.byref(cfg) if cfg is not None else None), "moe_set_routing")
+
+
+def moe_experts_mx_bytes(layer: int, fmt: int) -> int:
+    return int(lib().moe_experts_mx_bytes(layer, fmt))
+
+
+def moe_prepare_experts_mx(layer: int, fmt: int, w1_exp: int, w2_exp: int, buffer: Optional[int], nbytes: int,
+                           stream: int) -> int:
+    return _check(lib().moe_prepare_experts_mx(layer, fmt, w1_exp, w2_exp, buffer, nbytes, stream),
+                  "moe_prepare_experts_mx")
+
+
 MOE_TIMING_EVENTS = 8
 STAGES = ("router", "dispatch", "scatter", "gemm1", "gemm2", "combine", "stats")
 
@@ -412,6 +433,34 @@ class MoELayer:
             self._planes = torch.empty(n, dtype=torch.uint8, device=self.device)
         s = stream if stream is not None else torch.cuda.current_stream(self.device).cuda_stream
         moe_prepare_router(self.handle, self._planes.data_ptr(), self._planes.numel(), s)
+
+    def set_routing(self, cfg):
+        """Route as an operators.RouteConfig says (moe_set_routing); None returns to
+        the router's own selection."""
+        import torch
+        moe_set_routing(self.handle, None if cfg is None else cfg._c[torch.float32])
+
+    def prepare_experts_mx(self, fmt: Optional[str] = "mxfp4", w1_exp: Optional[int] = None,
+                           w2_exp: Optional[int] = None, stream=None):
+        """Run the experts in 4 bits (moe_prepare_experts_mx): w1 and w2 are quantised
+        into a buffer this object keeps. The exponents of "nvfp4" weights are those of
+        weights of variance 1 / fan-in unless given. fmt None returns to bf16. Call it
+        between forwards, and again after changing the weights; StepGraphs and
+        HostPipelines made before it keep what they were captured with, and must not
+        be used any more."""
+        import math
+        import torch
+        s = stream if stream is not None else torch.cuda.current_stream(self.device).cuda_stream
+        if fmt is None:
+            moe_prepare_experts_mx(self.handle, 0, 0, 0, None, 0, s)
+            self._mx = None
+            return
+        exps = [e if e is not None else (round(-0.5 * math.log2(n)) if fmt == "nvfp4" else 0)
+                for e, n in ((w1_exp, self.w.d), (w2_exp, self.w.F))]
+        n = moe_experts_mx_bytes(self.handle, MOE_MX[fmt])
+        buf = torch.empty(max(n, 256), dtype=torch.uint8, device=self.device)
+        moe_prepare_experts_mx(self.handle, MOE_MX[fmt], exps[0], exps[1], buf.data_ptr(), buf.numel(), s)
+        self._mx = buf
 
     def workspace(self, T: int):
         import torch

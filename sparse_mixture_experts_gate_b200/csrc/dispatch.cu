@@ -82,7 +82,7 @@ __device__ __forceinline__ void dispatch_scan(const DispatchArgs &a) {
             }
         }
         kept = (int64_t)pre < a.C ? pre : (int)a.C;
-        padded = (kept + kRowBlock - 1) / kRowBlock * kRowBlock;
+        padded = (kept + a.row_block - 1) / a.row_block * a.row_block;
         tiles = (padded + kTokTile - 1) / kTokTile;
         nars = (padded + kNarrowTile - 1) / kNarrowTile;
     }

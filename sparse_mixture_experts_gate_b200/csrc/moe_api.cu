@@ -13,6 +13,8 @@
 #include "moe.h"
 #include "moe_common.cuh"
 #include "moe_kernels.cuh"
+#include "mx_common.cuh"
+#include "route_scores.cuh"
 
 using namespace moe;
 
@@ -80,6 +82,23 @@ bool encode_bf16_store(CUtensorMap *m, const void *base, uint64_t inner, uint64_
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+}  // namespace
+
+namespace moe {
+bool encode_mx_maps(MxMaps *m, int format, const void *a_codes, const void *a_scales, uint64_t rows, const void *w_codes,
+                    const void *w_scales, uint64_t groups, int n, int k) {
+    const int block = format == MOE_MX_MXFP4 ? 32 : 16;
+    const uint64_t tiles = mx_scale_tiles(k, block);
+    const uint32_t box = 256 / (4 * block);
+    return encode_u8_2d(&m->w, w_codes, k / 2, groups * n, 128) && encode_u8_2d(&m->a, a_codes, k / 2, rows, 16) &&
+           encode_u8_2d(&m->a96, a_codes, k / 2, rows, 96) &&
+           encode_scale_tiles(&m->sw, w_scales, tiles, groups * ((n + 127) / 128), box) &&
+           encode_scale_tiles(&m->sa, a_scales, tiles, (rows + 127) / 128, box);
+}
+}  // namespace moe
+
+namespace {
+
 struct Plan {
     int T = 0;
     int64_t C = 0;
@@ -91,6 +110,7 @@ struct Plan {
     size_t o_ctrl, o_rcnt, o_logits, o_idx, o_gates, o_slot, o_rowof, o_lse, o_psum, o_ccount, o_cbase, o_cpre, o_ckept,
         o_gstart, o_grows, o_bgroup, o_toktiles, o_narrowtiles, o_tiledone, o_rowassign, o_wsplit, o_xp, o_h, o_o, o_credit, o_partials,
         o_prestart, o_gsorted, o_rownorm, o_gz;
+    size_t o_mxtok, o_mxself, o_mxx, o_mxxs, o_mxh, o_mxhs;  // 4-bit experts: row maps, codes and scales of x and H
     size_t total = 0;
 };
 
@@ -142,6 +162,11 @@ struct moe_layer {
     int selftest_skip_stage = -1;  // moe_selftest_gemm_timeout only: GEMM 1's skipped stage
     int selftest_router_skip = -1;  // moe_selftest_router_timeout only: the fused router's skipped stage
     void *planes = nullptr;        // moe_prepare_router's persistent bf16 planes of the router matrix, or null
+    bool routed = false;           // moe_set_routing: `route` instead of the router's own selection
+    moe_route_config_t route;
+    int mx = -1;                   // moe_prepare_experts_mx: the experts' 4-bit format, or -1
+    int mx_exp[2] = {0, 0};        // and of both weight stacks the power of two, codes and scales
+    const uint8_t *mx_codes[2] = {nullptr, nullptr}, *mx_scales[2] = {nullptr, nullptr};
     CUtensorMap map_w1, map_w2;
     CUtensorMap map_w1h, map_w2h;  // the same with boxes of 64 rows (transposed last feature tiles)
     // State of the most recent forward, read by moe_aux_stats.
@@ -168,7 +193,14 @@ int64_t capacity_of(const moe_config_t &c, int T) {
 // tiles are short anyway (decode-sized batches).
 bool narrow_gemm(const moe_layer *L, int T) {
     const moe_config_t &c = L->cfg;
-    return L->tc && (int64_t)c.num_active * T <= (int64_t)kNarrowTile * c.num_experts;
+    return L->tc && L->mx < 0 && (int64_t)c.num_active * T <= (int64_t)kNarrowTile * c.num_experts;
+}
+
+// Segments of the row space begin at multiples of this: 4-bit experts' on a scale tile.
+int row_block(const moe_layer &L) { return L.mx >= 0 ? 128 : kRowBlock; }
+
+size_t mx_scales_bytes(int format, int64_t rows, int cols) {
+    return (size_t)((rows + 127) / 128) * mx_scale_tiles(cols, format == MOE_MX_MXFP4 ? 32 : 16) * 512;
 }
 
 Plan make_plan(const moe_layer &L, int T) {
@@ -178,10 +210,11 @@ Plan make_plan(const moe_layer &L, int T) {
     p.C = capacity_of(c, T);
     const int E = c.num_experts, k = c.num_active, S = c.num_shared;
     const int64_t kept_max = std::min<int64_t>((int64_t)k * T, (int64_t)E * p.C);
-    const int64_t routed = std::min<int64_t>(round_up(kept_max + (int64_t)E * (kRowBlock - 1), kRowBlock),
-                                             (int64_t)E * round_up(p.C, kRowBlock));
+    const int rb = row_block(L);
+    const int64_t routed =
+        std::min<int64_t>(round_up(kept_max + (int64_t)E * (rb - 1), rb), (int64_t)E * round_up(p.C, rb));
     p.R_routed_max = (int)routed;
-    p.T_pad = (int)round_up(T, kRowBlock);
+    p.T_pad = (int)round_up(T, rb);
     p.R_max = p.R_routed_max + S * p.T_pad;
     p.max_row_blocks = p.R_max / kRowBlock;
     // Each expert's segment splits into ceil(rows / 256) token tiles of >= 32 rows.
@@ -238,7 +271,14 @@ Plan make_plan(const moe_layer &L, int T) {
     p.o_wsplit = take(tc ? (size_t)router_fused_epad(E_tc) * 3 * c.input_dim * 2 : 0);
     p.o_gz = take(c.use_mlp_gater ? (size_t)T * c.gater_hidden_dim * 4 : 0);
     p.o_lpart = take(pieces > 1 ? (size_t)p.n_mtiles * 256 * router_fused_epad(E_tc) * p.ksplit * 4 : 0);
-    p.o_xp = take(c.dtype == MOE_DTYPE_BF16 ? (size_t)p.R_routed_max * c.input_dim * es : 0);
+    const bool mx = L.mx >= 0;
+    p.o_xp = take(c.dtype == MOE_DTYPE_BF16 && !mx ? (size_t)p.R_routed_max * c.input_dim * es : 0);
+    p.o_mxtok = take(mx ? (size_t)p.R_max * 4 : 0);
+    p.o_mxself = take(mx ? (size_t)p.R_max * 4 : 0);
+    p.o_mxx = take(mx ? (size_t)p.R_max * c.input_dim / 2 : 0);
+    p.o_mxxs = take(mx ? mx_scales_bytes(L.mx, p.R_max, c.input_dim) : 0);
+    p.o_mxh = take(mx ? (size_t)p.R_max * c.expert_dim / 2 : 0);
+    p.o_mxhs = take(mx ? mx_scales_bytes(L.mx, p.R_max, c.expert_dim) : 0);
     p.o_h = take((size_t)p.R_max * c.expert_dim * es);
     p.o_o = take((size_t)p.R_max * c.output_dim * es);
     p.total = off;
@@ -406,6 +446,24 @@ int64_t moe_capacity(const moe_layer_t *layer, int32_t T) {
 
 namespace {
 
+// Rows of bf16 `x` to the layer's 4-bit format, into the workspace.
+cudaError_t quantize_rows(moe_layer *L, const void *x, int x_rows, int cols, const int32_t *row_index, size_t o_codes,
+                          size_t o_scales, cudaStream_t s) {
+    MxQuantArgs a;
+    a.x = x;
+    a.ld = cols;
+    a.x_rows = x_rows;
+    a.row_index = row_index;
+    a.rows = L->plan.R_max;
+    a.cols = cols;
+    a.pre = a.post = 1.f;
+    a.codes = reinterpret_cast<uint8_t *>(L->ws + o_codes);
+    a.scales = reinterpret_cast<uint8_t *>(L->ws + o_scales);
+    a.values = nullptr;
+    a.values_ld = 0;
+    return launch_mx_quantize(a, L->mx, true, L->num_sms, s);
+}
+
 // Router, dispatch and row scatter of one forward (everything before the
 // expert GEMMs); records what the later phases need in the layer.
 int fwd_route(moe_layer_t *L, const void *x, int32_t T, const float *logit_noise, void *workspace, size_t ws_bytes,
@@ -538,6 +596,19 @@ int fwd_route(moe_layer_t *L, const void *x, int32_t T, const float *logit_noise
     } else {
         MOE_LAUNCH(launch_router(ra, s, nl));
     }
+    if (L->routed) {  // the selection and the gates from the router's logits
+        RouteArgs sa = route_args(L->route);
+        sa.logits = logits;
+        sa.ld = E;
+        sa.T = T;
+        sa.bias = c.use_selection_bias ? L->w.sel_bias : nullptr;
+        sa.weights = gates;
+        sa.idx = idx;
+        sa.counts = nullptr;
+        sa.fill = 1;  // the dispatch needs an expert for every choice
+        MOE_LAUNCH(launch_route(sa, false, L->num_sms, s));
+        ++*nl;
+    }
     MOE_MARK(L, 1, s);
     if (router_only) return MOE_OK;
 
@@ -551,6 +622,7 @@ int fwd_route(moe_layer_t *L, const void *x, int32_t T, const float *logit_noise
     da.S = S;
     da.C = p.C;
     da.T_pad = p.T_pad;
+    da.row_block = row_block(*L);
     da.n_chunks = p.n_chunks;
     da.chunk_count = reinterpret_cast<int32_t *>(ws + p.o_ccount);
     da.chunk_base = reinterpret_cast<int32_t *>(ws + p.o_cbase);
@@ -575,7 +647,22 @@ int fwd_route(moe_layer_t *L, const void *x, int32_t T, const float *logit_noise
     MOE_LAUNCH(launch_dispatch(da, s, nl));
     MOE_MARK(L, 2, s);
 
-    if (L->tc) {
+    if (L->mx >= 0) {
+        MxRowMapArgs ma;
+        ma.row_assign = da.row_assign;
+        ma.group_start = da.group_start;
+        ma.E = E;
+        ma.S = S;
+        ma.k = k;
+        ma.T = T;
+        ma.T_pad = p.T_pad;
+        ma.rows = p.R_max;
+        ma.token = reinterpret_cast<int32_t *>(ws + p.o_mxtok);
+        ma.self = reinterpret_cast<int32_t *>(ws + p.o_mxself);
+        MOE_LAUNCH(launch_mx_row_map(ma, s));
+        MOE_LAUNCH(quantize_rows(L, x, T, c.input_dim, ma.token, p.o_mxx, p.o_mxxs, s));
+        *nl += 2;
+    } else if (L->tc) {
         ScatterArgs sa;
         sa.x = x;
         sa.xp = ws + p.o_xp;
@@ -608,7 +695,42 @@ int fwd_expert_gemms(moe_layer_t *L, cudaStream_t s, bool shared_only) {
     da.block_group = reinterpret_cast<int32_t *>(ws + p.o_bgroup);
     da.row_assign = reinterpret_cast<int32_t *>(ws + p.o_rowassign);
 
-    if (L->tc) {
+    if (L->mx >= 0) {
+        // 4-bit experts: layer 1 on the quantised tokens, its bf16 hidden rows quantised, layer 2.
+        const uint8_t *xc[2] = {reinterpret_cast<uint8_t *>(ws + p.o_mxx), reinterpret_cast<uint8_t *>(ws + p.o_mxh)};
+        const uint8_t *xs[2] = {reinterpret_cast<uint8_t *>(ws + p.o_mxxs), reinterpret_cast<uint8_t *>(ws + p.o_mxhs)};
+        const int in[2] = {c.input_dim, c.expert_dim}, out[2] = {c.expert_dim, c.output_dim};
+        for (int l = 0; l < 2; ++l) {
+            if (l == 1) {
+                MOE_LAUNCH(quantize_rows(L, ws + p.o_h, p.R_max, c.expert_dim,
+                                         reinterpret_cast<int32_t *>(ws + p.o_mxself), p.o_mxh, p.o_mxhs, s));
+                ++*nl;
+            }
+            MxGemmArgs g;
+            g.group_start = da.group_start;
+            g.group_rows = da.group_rows;
+            g.rows = p.R_max;
+            g.N = out[l];
+            g.K = in[l];
+            g.G = E + S;
+            g.filled = (int64_t)k * T + (int64_t)S * T;
+            g.bias = l ? L->w.b2 : L->w.b1;
+            g.alpha = nullptr;
+            g.post = std::ldexp(1.f, L->mx_exp[l]);
+            g.act = l ? -1 : c.activation;
+            g.out = ws + (l ? p.o_o : p.o_h);
+            g.out_f32 = 0;
+            g.out_ld = out[l];
+            g.vec_ok = 1;
+            g.status = status;
+            MxMaps m;
+            if (!encode_mx_maps(&m, L->mx, xc[l], xs[l], p.R_max, L->mx_codes[l], L->mx_scales[l], E + S, out[l], in[l]))
+                return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the 4-bit experts");
+            MOE_LAUNCH(launch_mx_gemm(m, g, L->mx, L->num_sms, s));
+            ++*nl;
+            MOE_MARK(L, 4 + l, s);
+        }
+    } else if (L->tc) {
         PairGemmArgs g1;
         g1.tok_tiles = da.tok_tiles;
         g1.group_start = da.group_start;
@@ -1109,12 +1231,104 @@ int moe_prepare_router(moe_layer_t *L, void *planes, size_t bytes, void *stream_
     return MOE_OK;
 }
 
+int moe_set_routing(moe_layer_t *L, const moe_route_config_t *cfg) {
+    g_last_error.clear();
+    if (!L) return fail(MOE_ERR_INVALID_ARG, "layer is NULL");
+    if (!cfg) {
+        L->routed = false;
+        return MOE_OK;
+    }
+    const int rc = check_route_config(cfg);
+    if (rc != MOE_OK) return rc;
+    if (cfg->num_experts != L->cfg.num_experts || cfg->num_active != L->cfg.num_active)
+        return fail(MOE_ERR_INVALID_ARG, "the routing has %d experts, %d active; the layer %d and %d", cfg->num_experts,
+                    cfg->num_active, L->cfg.num_experts, L->cfg.num_active);
+    if (cfg->dtype != MOE_DTYPE_FP32) return fail(MOE_ERR_INVALID_ARG, "the layer's router logits are FP32");
+    if (L->cfg.top_k_method != MOE_TOPK_GREEDY)
+        return fail(MOE_ERR_UNSUPPORTED, "NOISY top-k adds noise to the logits: it has no form with scores");
+    L->route = *cfg;
+    L->routed = true;
+    return MOE_OK;
+}
+
+namespace {
+struct MxWeights {
+    size_t codes[2], scales[2], total;
+};
+MxWeights mx_weights(const moe_layer &L, int format) {
+    const moe_config_t &c = L.cfg;
+    const int n[2] = {c.expert_dim, c.output_dim}, k[2] = {c.input_dim, c.expert_dim};
+    MxWeights w;
+    w.total = 0;
+    for (int l = 0; l < 2; ++l) {
+        w.codes[l] = w.total;
+        w.total = align_up(w.total + (size_t)L.G * n[l] * (k[l] / 2), 256);
+        w.scales[l] = w.total;
+        w.total = align_up(w.total + (size_t)L.G * mx_scales_bytes(format, n[l], k[l]), 256);
+    }
+    return w;
+}
+}  // namespace
+
+size_t moe_experts_mx_bytes(const moe_layer_t *L, int32_t format) {
+    if (!L || !L->tc || (format != MOE_MX_MXFP4 && format != MOE_MX_NVFP4)) return 0;
+    return mx_weights(*L, format).total;
+}
+
+int moe_prepare_experts_mx(moe_layer_t *L, int32_t format, int32_t w1_exp, int32_t w2_exp, void *buffer, size_t bytes,
+                           void *stream_v) {
+    g_last_error.clear();
+    if (!L) return fail(MOE_ERR_INVALID_ARG, "layer is NULL");
+    if (!buffer) {
+        if (L->mx >= 0) L->has_forward = false;  // its workspace has the other layout
+        L->mx = -1;
+        return MOE_OK;
+    }
+    if (format != MOE_MX_MXFP4 && format != MOE_MX_NVFP4) return fail(MOE_ERR_INVALID_ARG, "unknown format %d", format);
+    if (!L->tc) return fail(MOE_ERR_UNSUPPORTED, "4-bit experts are made of bf16 layers");
+    if (L->cfg.ep_size > 1) return fail(MOE_ERR_UNSUPPORTED, "4-bit experts are not offered for ep_size > 1");
+    if (w1_exp < -60 || w1_exp > 60 || w2_exp < -60 || w2_exp > 60)
+        return fail(MOE_ERR_INVALID_ARG, "w1_exp and w2_exp must be in -60..60 (got %d, %d)", w1_exp, w2_exp);
+    const MxWeights w = mx_weights(*L, format);
+    if (bytes < w.total) return fail(MOE_ERR_WORKSPACE, "4-bit experts: %zu bytes given, %zu needed", bytes, w.total);
+    if (reinterpret_cast<uintptr_t>(buffer) % 256) return fail(MOE_ERR_WORKSPACE, "buffer must be 256-byte aligned");
+    const moe_config_t &c = L->cfg;
+    const int n[2] = {c.expert_dim, c.output_dim}, k[2] = {c.input_dim, c.expert_dim}, e[2] = {w1_exp, w2_exp};
+    const void *src[2] = {L->w.w1, L->w.w2};
+    uint8_t *to = static_cast<uint8_t *>(buffer);
+    cudaStream_t s = as_stream(stream_v);
+    for (int l = 0; l < 2; ++l)
+        for (int g = 0; g < L->G; ++g) {
+            MxQuantArgs a;
+            a.x = static_cast<const __nv_bfloat16 *>(src[l]) + (size_t)g * n[l] * k[l];
+            a.ld = k[l];
+            a.x_rows = a.rows = n[l];
+            a.row_index = nullptr;
+            a.cols = k[l];
+            a.pre = std::ldexp(1.f, -e[l]);
+            a.post = std::ldexp(1.f, e[l]);
+            a.codes = to + w.codes[l] + (size_t)g * n[l] * (k[l] / 2);
+            a.scales = to + w.scales[l] + (size_t)g * mx_scales_bytes(format, n[l], k[l]);
+            a.values = nullptr;
+            a.values_ld = 0;
+            MOE_LAUNCH(launch_mx_quantize(a, format, true, L->num_sms, s));
+        }
+    for (int l = 0; l < 2; ++l) {
+        L->mx_codes[l] = to + w.codes[l];
+        L->mx_scales[l] = to + w.scales[l];
+        L->mx_exp[l] = e[l];
+    }
+    if (L->mx < 0) L->has_forward = false;
+    L->mx = format;
+    return MOE_OK;
+}
+
 int moe_selftest_gemm_timeout(moe_layer_t *L, const void *x, int32_t T, void *workspace, size_t ws_bytes, void *y,
                               void *stream_v) {
     g_last_error.clear();
     if (!L) return fail(MOE_ERR_INVALID_ARG, "layer is NULL");
-    if (!L->tc || L->cfg.ep_size > 1)
-        return fail(MOE_ERR_UNSUPPORTED, "the self-test runs the tensor-core expert GEMM of a bf16 layer, ep_size 1");
+    if (!L->tc || L->cfg.ep_size > 1 || L->mx >= 0)
+        return fail(MOE_ERR_UNSUPPORTED, "the self-test runs the bf16 tensor-core expert GEMM, ep_size 1");
     if (L->cfg.top_k_method != MOE_TOPK_GREEDY) return fail(MOE_ERR_UNSUPPORTED, "the self-test needs GREEDY top-k");
     if (T <= 0) return fail(MOE_ERR_INVALID_ARG, "the self-test needs T > 0");
     if (L->cfg.input_dim < 3 * kBK)

@@ -78,7 +78,8 @@ struct DispatchArgs {
     int rank_major;         // capacity priority: 0 token order, 1 choice by choice (item = r T + t)
     int n_items;            // T (token order) or k T (rank-major)
     int64_t C;              // capacity
-    int T_pad;              // T rounded up to kRowBlock (shared-expert segment length)
+    int T_pad;              // T rounded up to row_block (shared-expert segment length)
+    int row_block = kRowBlock;  // every segment's rows are padded to a multiple (of kRowBlock too)
     int n_chunks;           // ceil(n_items / 256)
     int32_t *chunk_count;   // [n_chunks][E]
     int32_t *chunk_base;    // [n_chunks][E]

@@ -43,6 +43,17 @@ struct MxQuantArgs {
 };
 cudaError_t launch_mx_quantize(const MxQuantArgs &a, int format, bool bf16, int num_sms, cudaStream_t s);
 
+// Source rows for the rows of a layer's row space: `token` [rows] is the token of
+// each kept assignment's row and of each shared expert's row, `self` the row itself;
+// -1 for rows that hold nothing.
+struct MxRowMapArgs {
+    const int32_t *row_assign;   // [routed rows] t k + r, or -1
+    const int32_t *group_start;  // [E + S + 1]
+    int E, S, k, T, T_pad, rows;
+    int32_t *token, *self;
+};
+cudaError_t launch_mx_row_map(const MxRowMapArgs &a, cudaStream_t s);
+
 struct MxDequantArgs {
     const uint8_t *codes, *scales;
     int rows, cols;
@@ -55,6 +66,7 @@ cudaError_t launch_mx_dequantize(const MxDequantArgs &a, int format, bool bf16, 
 struct MxGemmArgs {
     const int32_t *group_start, *group_rows;  // [G] or null (one group of all rows)
     int rows, N, K, G;
+    int64_t filled;      // about how many of the rows belong to groups
     const float *bias;   // [G][N] or null
     const float *alpha;  // [G] or null
     float post;          // 2^scale_exp of both operands
@@ -70,6 +82,8 @@ struct MxGemmArgs {
 struct MxMaps {
     CUtensorMap w, a, a96, sw, sa;
 };
+bool encode_mx_maps(MxMaps *m, int format, const void *a_codes, const void *a_scales, uint64_t rows, const void *w_codes,
+                    const void *w_scales, uint64_t groups, int n, int k);
 cudaError_t launch_mx_gemm(const MxMaps &m, const MxGemmArgs &a, int format, int num_sms, cudaStream_t s);
 
 // Device status bits the product adds to kDevTimeout.

@@ -303,6 +303,22 @@ __global__ void __launch_bounds__(kThreads) mx_dequantize_kernel(const MxDequant
     store8<OT>(static_cast<OT *>(a.out) + r * a.ld + c, vec, o);
 }
 
+__global__ void __launch_bounds__(kThreads) mx_row_map_kernel(const MxRowMapArgs a) {
+    const int r = blockIdx.x * kThreads + threadIdx.x;
+    if (r >= a.rows) return;
+    const int routed = a.group_start[a.E];
+    int token = -1;
+    if (r < routed) {
+        const int as = a.row_assign[r];
+        if (as >= 0) token = as / a.k;
+    } else if (a.T_pad > 0 && (r - routed) / a.T_pad < a.S) {
+        const int t = (r - routed) % a.T_pad;
+        if (t < a.T) token = t;
+    }
+    a.token[r] = token;
+    a.self[r] = token >= 0 ? r : -1;
+}
+
 bool vector_rows(const void *p, int64_t ld, int elem, int bytes) {
     return reinterpret_cast<uintptr_t>(p) % bytes == 0 && ld * elem % bytes == 0;
 }
@@ -334,6 +350,11 @@ cudaError_t launch_mx_quantize(const MxQuantArgs &a, int format, bool bf16, int 
     if (format == kMxFp4)
         return bf16 ? quantize<kMxFp4, __nv_bfloat16, 2>(a, num_sms, s) : quantize<kMxFp4, float, 1>(a, num_sms, s);
     return bf16 ? quantize<kNvFp4, __nv_bfloat16, 2>(a, num_sms, s) : quantize<kNvFp4, float, 1>(a, num_sms, s);
+}
+
+cudaError_t launch_mx_row_map(const MxRowMapArgs &a, cudaStream_t s) {
+    mx_row_map_kernel<<<(a.rows + kThreads - 1) / kThreads, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_mx_dequantize(const MxDequantArgs &a, int format, bool bf16, cudaStream_t s) {

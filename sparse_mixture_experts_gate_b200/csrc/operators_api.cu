@@ -53,7 +53,10 @@ int launched(cudaError_t e, const char *what) {
     return e == cudaSuccess ? MOE_OK : fail(MOE_ERR_CUDA, "%s failed: %s", what, cudaGetErrorString(e));
 }
 
-int check_route(const moe_route_config_t *c) {
+}  // namespace
+
+namespace moe {
+int check_route_config(const moe_route_config_t *c) {
     if (!c) return fail(MOE_ERR_INVALID_ARG, "cfg is NULL");
     if (c->num_experts < 1) return fail(MOE_ERR_INVALID_ARG, "num_experts must be >= 1 (got %d)", c->num_experts);
     if (c->num_experts > kRouteMaxExperts)
@@ -84,6 +87,22 @@ int check_route(const moe_route_config_t *c) {
         return fail(MOE_ERR_INVALID_ARG, "unknown dtype %d", c->dtype);
     return MOE_OK;
 }
+
+RouteArgs route_args(const moe_route_config_t &c) {
+    RouteArgs a;
+    a.E = c.num_experts;
+    a.k = c.num_active;
+    a.sigmoid = c.score == MOE_SCORE_SIGMOID;
+    a.groups = c.num_groups;
+    a.top_groups = c.top_groups;
+    a.group_top = c.group_top;
+    a.renormalize = c.renormalize;
+    a.scale = c.scale;
+    return a;
+}
+}  // namespace moe
+
+namespace {
 
 int check_rows(const moe_route_config_t *c, const void *logits, int64_t ld, int32_t T, const char *name) {
     const size_t es = c->dtype == MOE_DTYPE_BF16 ? 2 : 4;
@@ -131,7 +150,7 @@ moe_route_config_t moe_route_config_default(void) {
 int moe_route(const moe_route_config_t *cfg, const void *logits, int64_t ld, int32_t T, const float *bias,
               float *weights, int32_t *topk_idx, int32_t *counts, void *stream_v) {
     report_error(MOE_OK, "");
-    int rc = check_route(cfg);
+    int rc = check_route_config(cfg);
     if (rc != MOE_OK) return rc;
     if (T < 0) return fail(MOE_ERR_INVALID_ARG, "T must be >= 0 (got %d)", T);
     if ((rc = check_rows(cfg, logits, ld, T, "logits")) != MOE_OK) return rc;
@@ -140,18 +159,10 @@ int moe_route(const moe_route_config_t *cfg, const void *logits, int64_t ld, int
         return fail(MOE_ERR_INVALID_ARG, "arrays must be 4-byte aligned");
     int sms = 0;
     if ((rc = device_sms(&sms)) != MOE_OK) return rc;
-    RouteArgs a;
+    RouteArgs a = route_args(*cfg);
     a.logits = logits;
     a.ld = ld;
     a.T = T;
-    a.E = cfg->num_experts;
-    a.k = cfg->num_active;
-    a.sigmoid = cfg->score == MOE_SCORE_SIGMOID;
-    a.groups = cfg->num_groups;
-    a.top_groups = cfg->top_groups;
-    a.group_top = cfg->group_top;
-    a.renormalize = cfg->renormalize;
-    a.scale = cfg->scale;
     a.bias = bias;
     a.weights = weights;
     a.idx = topk_idx;
@@ -162,7 +173,7 @@ int moe_route(const moe_route_config_t *cfg, const void *logits, int64_t ld, int
 int moe_route_backward(const moe_route_config_t *cfg, const float *grad_weights, const void *logits, int64_t ld,
                        const int32_t *topk_idx, int32_t T, void *grad_logits, int64_t grad_ld, void *stream_v) {
     report_error(MOE_OK, "");
-    int rc = check_route(cfg);
+    int rc = check_route_config(cfg);
     if (rc != MOE_OK) return rc;
     if (T < 0) return fail(MOE_ERR_INVALID_ARG, "T must be >= 0 (got %d)", T);
     if ((rc = check_rows(cfg, logits, ld, T, "logits")) != MOE_OK) return rc;
@@ -302,13 +313,7 @@ int moe_mx_gemm(const moe_mx_gemm_t *p, void *stream_v) {
     int sms = 0;
     if ((rc = device_sms(&sms)) != MOE_OK) return rc;
     MxMaps m;
-    const uint64_t tiles = mx_scale_tiles(p->k, block_of(p->format));
-    if (!encode_u8_2d(&m.w, p->w_codes, p->k / 2, (uint64_t)p->groups * p->n, 128) ||
-        !encode_u8_2d(&m.a, p->a_codes, p->k / 2, p->rows, 16) ||
-        !encode_u8_2d(&m.a96, p->a_codes, p->k / 2, p->rows, 96) ||
-        !encode_scale_tiles(&m.sw, p->w_scales, tiles, (uint64_t)p->groups * ((p->n + 127) / 128),
-                            256 / (4 * block_of(p->format))) ||
-        !encode_scale_tiles(&m.sa, p->a_scales, tiles, ((uint64_t)p->rows + 127) / 128, 256 / (4 * block_of(p->format))))
+    if (!encode_mx_maps(&m, p->format, p->a_codes, p->a_scales, p->rows, p->w_codes, p->w_scales, p->groups, p->n, p->k))
         return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the codes or scales");
     MxGemmArgs a;
     a.group_start = p->group_start;
@@ -326,6 +331,8 @@ int moe_mx_gemm(const moe_mx_gemm_t *p, void *stream_v) {
     a.out_ld = p->out_ld;
     a.vec_ok = !a.out_f32 && aligned(p->out, 16) && p->out_ld % 8 == 0;
     a.status = p->status;
+    // Rows beyond the 127 that each group's start may leave unused.
+    a.filled = (int64_t)p->rows - (p->groups > 1 ? (int64_t)p->groups * 127 : 0);
     return launched(launch_mx_gemm(m, a, p->format, sms, as_stream(stream_v)), "moe_mx_gemm");
 }
 

@@ -434,6 +434,14 @@ __global__ void __launch_bounds__(kThreads, RE > 8 ? 2 : 3) route_kernel(const _
         }
     };
     auto write = [&](int64_t t, int choice, float weight) {
+        if (a.fill && __any_sync(0xffffffffu, lane < a.k && choice < 0)) {
+            int n = __popc(__ballot_sync(0xffffffffu, lane < a.k && choice >= 0));  // the choices there are
+            for (int e = 0; n < a.k && e < a.E; ++e)
+                if (!__any_sync(0xffffffffu, lane < a.k && choice == e)) {
+                    if (lane == n) choice = e;
+                    ++n;
+                }
+        }
         if (lane < a.k) {
             a.idx[t * a.k + lane] = choice;
             a.weights[t * a.k + lane] = weight;

@@ -1,6 +1,7 @@
 // route_scores.cuh - argument blocks of the routing operator (route_scores.cu).
 #pragma once
 
+#include "moe.h"
 #include "moe_common.cuh"
 
 namespace moe {
@@ -20,8 +21,12 @@ struct RouteArgs {
     const float *bias;   // [E] or null
     float *weights;      // [T][k]
     int32_t *idx;        // [T][k]
-    int32_t *counts;     // [E], zero, or null
+    int32_t *counts;     // [E] or null
+    int fill = 0;        // 1: choices that are left over take the lowest free experts (weight 0) instead of -1
 };
+// Checks a configuration (sets the last error); its part of the arguments.
+int check_route_config(const moe_route_config_t *c);
+RouteArgs route_args(const moe_route_config_t &c);
 cudaError_t launch_route(const RouteArgs &a, bool bf16, int num_sms, cudaStream_t s);
 
 struct RouteBackwardArgs {

@@ -111,6 +111,13 @@ def test_product_refusals(L):
     assert L.moe_mx_gemm(ctypes.byref(B.MoeMxGemm(**{**ok, "rows": 0})), None) == B.MOE_OK
 
 
+def test_layer_calls_without_a_layer(L):
+    c = B.moe_route_config_default()
+    assert L.moe_set_routing(None, ctypes.byref(c)) == B.MOE_ERR_INVALID_ARG
+    assert L.moe_prepare_experts_mx(None, 0, 0, 0, P, 1 << 20, None) == B.MOE_ERR_INVALID_ARG
+    assert B.moe_experts_mx_bytes(None, 0) == 0
+
+
 def test_python_refusals():
     with pytest.raises(ValueError):
         ops.RouteConfig(8, 2, score="tanh")

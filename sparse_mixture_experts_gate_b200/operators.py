@@ -9,6 +9,7 @@ current stream of its tensors' device; nothing is differentiable through autogra
 """
 from __future__ import annotations
 
+import ctypes
 from typing import Optional, Tuple
 
 import torch
@@ -17,20 +18,26 @@ from . import binding as B
 
 _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
 _BLOCK = {"mxfp4": 32, "nvfp4": 16}
-_current_device = torch.cuda.current_device
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
     lambda device: torch.cuda.current_stream(device).cuda_stream
+_current = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
-def _call(t: torch.Tensor, fn, *args):
-    """fn(*args, the current stream of t's device) with that device current."""
-    device = t.device.index
-    if device is None or not t.is_cuda:
+def _call(device: int, where: str, fn, *args):
+    """fn(*args, the current stream of `device`) with that device current."""
+    if device < 0:
         raise ValueError("the operators take CUDA tensors")
-    if device == _current_device():
-        return fn(*args, _raw_stream(device))
-    with torch.cuda.device(device):
-        return fn(*args, _raw_stream(device))
+    if device == _current():
+        rc = fn(*args, _raw_stream(device))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, _raw_stream(device))
+    if rc:
+        raise B.MoEError(rc, where, B.moe_last_error())
+
+
+# Contiguous tensors; of the ways to make them the one that takes the least host time.
+_empty = torch.empty_strided
 
 
 def _rows(name: str, t: torch.Tensor, cols: Optional[int] = None) -> int:
@@ -49,7 +56,8 @@ def _rows(name: str, t: torch.Tensor, cols: Optional[int] = None) -> int:
 
 def _array(name: str, t: torch.Tensor, like: torch.Tensor, dtype, shape=None) -> int:
     """The address of a contiguous array."""
-    if t.dtype != dtype or not t.is_contiguous() or t.device != like.device or (shape is not None and t.shape != shape):
+    if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != like.get_device() or \
+            (shape is not None and t.shape != shape):
         raise ValueError(f"{name}: a contiguous {dtype} tensor{'' if shape is None else f' of {tuple(shape)}'} on "
                          f"{like.device} is needed, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
@@ -67,6 +75,7 @@ class RouteConfig:
         self.num_experts, self.num_active = num_experts, num_active
         self._c = {d: B.MoeRouteConfig(num_experts, num_active, B.MOE_SCORE[score], num_groups, top_groups, group_top,
                                        int(renormalize), scale, code) for d, code in _DTYPE.items()}
+        self._ref = {d: ctypes.byref(c) for d, c in self._c.items()}
 
 
 def route(logits: torch.Tensor, cfg: RouteConfig, bias: Optional[torch.Tensor] = None, counts: bool = True,
@@ -79,17 +88,17 @@ def route(logits: torch.Tensor, cfg: RouteConfig, bias: Optional[torch.Tensor] =
     T, dev = logits.shape[0], logits.device
     b = None if bias is None else _array("bias", bias, logits, torch.float32, (E,))
     if out is None:
-        w = torch.empty((T, k), dtype=torch.float32, device=dev)
-        idx = torch.empty((T, k), dtype=torch.int32, device=dev)
-        n = torch.empty((E,), dtype=torch.int32, device=dev) if counts else None
+        w = _empty((T, k), (k, 1), dtype=torch.float32, device=dev)
+        idx = _empty((T, k), (k, 1), dtype=torch.int32, device=dev)
+        n = _empty((E,), (1,), dtype=torch.int32, device=dev) if counts else None
     else:
         w, idx, n = out
         _array("weights", w, logits, torch.float32, (T, k))
         _array("topk_idx", idx, logits, torch.int32, (T, k))
         if n is not None:
             _array("counts", n, logits, torch.int32, (E,))
-    _call(logits, B.moe_route, cfg._c[logits.dtype], logits.data_ptr(), ld, T, b, w.data_ptr(), idx.data_ptr(),
-          None if n is None else n.data_ptr())
+    _call(logits.get_device(), "moe_route", B.lib().moe_route, cfg._ref[logits.dtype], logits.data_ptr(), ld, T, b,
+          w.data_ptr(), idx.data_ptr(), None if n is None else n.data_ptr())
     return w, idx, n
 
 
@@ -102,13 +111,14 @@ def route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, topk_idx: t
     g = _array("grad_weights", grad_weights, logits, torch.float32, shape)
     idx = _array("topk_idx", topk_idx, logits, torch.int32, shape)
     if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        out = _empty((T, cfg.num_experts), (cfg.num_experts, 1), dtype=logits.dtype, device=logits.device)
         out_ld = cfg.num_experts
     else:
         if out.dtype != logits.dtype or out.shape != logits.shape or out.device != logits.device:
             raise ValueError("out has to be like logits")
         out_ld = _rows("out", out)
-    _call(logits, B.moe_route_backward, cfg._c[logits.dtype], g, logits.data_ptr(), ld, idx, T, out.data_ptr(), out_ld)
+    _call(logits.get_device(), "moe_route_backward", B.lib().moe_route_backward, cfg._ref[logits.dtype], g,
+          logits.data_ptr(), ld, idx, T, out.data_ptr(), out_ld)
     return out
 
 
@@ -136,6 +146,9 @@ class MxTensor:
                               ("scales", scales, groups * _scale_bytes(fmt, rows, cols))):
             if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() < need or t.device != codes.device:
                 raise ValueError(f"{name}: at least {need} contiguous bytes on one device are needed")
+        self._set(fmt, codes, scales, rows, cols, groups, scale_exp)
+
+    def _set(self, fmt, codes, scales, rows, cols, groups, scale_exp):
         self.format, self.codes, self.scales = fmt, codes, scales
         self.rows, self.cols, self.groups, self.scale_exp = rows, cols, groups, scale_exp
 
@@ -158,6 +171,8 @@ def mx_quantize(x: torch.Tensor, fmt: str = "mxfp4", row_index: Optional[torch.T
     x_rows, cols = x.shape
     if fmt not in _BLOCK:
         raise ValueError(f"unknown format {fmt!r}")
+    if cols < 32 or cols % 32:
+        raise ValueError(f"a row needs a positive multiple of 32 elements, got {cols}")
     if row_index is None:
         rows, index = x_rows, None
     else:
@@ -168,14 +183,15 @@ def mx_quantize(x: torch.Tensor, fmt: str = "mxfp4", row_index: Optional[torch.T
             raise ValueError(f"values: {x.dtype} {(rows, cols)} on {x.device} is needed")
         v, v_ld = values.data_ptr(), _rows("values", values)
     if out is None:
-        codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=x.device)
-        scales = torch.empty((_scale_bytes(fmt, rows, cols),), dtype=torch.uint8, device=x.device)
-        out = MxTensor(fmt, codes, scales, rows, cols, 1, scale_exp)
+        codes = _empty((rows, cols // 2), (cols // 2, 1), dtype=torch.uint8, device=x.device)
+        scales = _empty((_scale_bytes(fmt, rows, cols),), (1,), dtype=torch.uint8, device=x.device)
+        out = MxTensor.__new__(MxTensor)
+        out._set(fmt, codes, scales, rows, cols, 1, scale_exp)
     elif (out.format, out.rows, out.cols, out.groups, out.scale_exp) != (fmt, rows, cols, 1, scale_exp) or \
             out.codes.device != x.device:
         raise ValueError("out has another format, size, exponent or device")
-    _call(x, B.moe_mx_quantize, B.MOE_MX[fmt], x.data_ptr(), _DTYPE[x.dtype], ld, x_rows, cols, index, rows, scale_exp,
-          out.codes.data_ptr(), out.scales.data_ptr(), v or None, v_ld)
+    _call(x.get_device(), "moe_mx_quantize", B.lib().moe_mx_quantize, B.MOE_MX[fmt], x.data_ptr(), _DTYPE[x.dtype], ld,
+          x_rows, cols, index, rows, scale_exp, out.codes.data_ptr(), out.scales.data_ptr(), v or None, v_ld)
     return out
 
 
@@ -186,8 +202,8 @@ def mx_dequantize(q: MxTensor, dtype: torch.dtype = torch.float32) -> torch.Tens
     if q.groups != 1:
         raise ValueError("one group at a time")
     out = torch.empty(q.rows, q.cols, dtype=dtype, device=q.codes.device)
-    _call(out, B.moe_mx_dequantize, B.MOE_MX[q.format], q.codes.data_ptr(), q.scales.data_ptr(), q.rows, q.cols,
-          q.scale_exp, out.data_ptr(), _DTYPE[dtype], q.cols)
+    _call(out.get_device(), "moe_mx_dequantize", B.lib().moe_mx_dequantize, B.MOE_MX[q.format], q.codes.data_ptr(),
+          q.scales.data_ptr(), q.rows, q.cols, q.scale_exp, out.data_ptr(), _DTYPE[dtype], q.cols)
     return out
 
 
@@ -225,12 +241,12 @@ def mx_gemm(a: MxTensor, w: MxTensor, group_start: Optional[torch.Tensor] = None
     else:
         raise ValueError(f"unknown activation {activation!r}")
     if out is None:
-        out = torch.empty((a.rows, n), dtype=dtype, device=like.device)
+        out = _empty((a.rows, n), (n, 1), dtype=dtype, device=like.device)
     elif out.device != like.device or out.shape[0] != a.rows:
         raise ValueError(f"out: {a.rows} rows on {like.device} are needed")
     ld = _rows("out", out, n)
     args = B.MoeMxGemm(B.MOE_MX[a.format], a.rows, n, a.cols, G, a.scale_exp + w.scale_exp, act, _DTYPE[out.dtype], ld,
                        like.data_ptr(), a.scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(), start, rows, b, al,
                        out.data_ptr(), st)
-    _call(like, B.moe_mx_gemm, args)
+    _call(like.get_device(), "moe_mx_gemm", B.lib().moe_mx_gemm, ctypes.byref(args))
     return out

@@ -473,6 +473,14 @@ MOE_API int moe_mx_quantize(int32_t format, const void *x, int32_t dtype, int64_
                             const int32_t *row_index, int32_t rows, int32_t scale_exp, void *codes, void *scales,
                             void *values, int64_t values_ld, void *stream);
 
+/* Gathers quantised rows: row r of out_codes and out_scales (rows x cols) becomes
+ * row row_index[r] of codes and scales (src_rows x cols), and is left as it was
+ * where that is outside 0..src_rows-1. The outputs may not overlap the inputs. With
+ * rows that are wanted several times this costs less than quantising each of
+ * them. Errors: INVALID_ARG, CUDA. */
+MOE_API int moe_mx_gather(int32_t format, const void *codes, const void *scales, int32_t src_rows, int32_t cols,
+                          const int32_t *row_index, int32_t rows, void *out_codes, void *out_scales, void *stream);
+
 /* The values of codes and scales, to `out` (dtype MOE_DTYPE_*, rows ld apart). */
 MOE_API int moe_mx_dequantize(int32_t format, const void *codes, const void *scales, int32_t rows, int32_t cols,
                               int32_t scale_exp, void *out, int32_t dtype, int64_t ld, void *stream);

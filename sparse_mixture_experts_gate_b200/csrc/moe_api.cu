@@ -110,7 +110,8 @@ struct Plan {
     size_t o_ctrl, o_rcnt, o_logits, o_idx, o_gates, o_slot, o_rowof, o_lse, o_psum, o_ccount, o_cbase, o_cpre, o_ckept,
         o_gstart, o_grows, o_bgroup, o_toktiles, o_narrowtiles, o_tiledone, o_rowassign, o_wsplit, o_xp, o_h, o_o, o_credit, o_partials,
         o_prestart, o_gsorted, o_rownorm, o_gz;
-    size_t o_mxtok, o_mxself, o_mxx, o_mxxs, o_mxh, o_mxhs;  // 4-bit experts: row maps, codes and scales of x and H
+    size_t o_mxtok, o_mxself, o_mxt, o_mxts, o_mxx, o_mxxs, o_mxh, o_mxhs;  // 4-bit experts: row maps; codes and scales of
+                                                                            // the tokens, their rows, and H
     size_t total = 0;
 };
 
@@ -275,6 +276,8 @@ Plan make_plan(const moe_layer &L, int T) {
     p.o_xp = take(c.dtype == MOE_DTYPE_BF16 && !mx ? (size_t)p.R_routed_max * c.input_dim * es : 0);
     p.o_mxtok = take(mx ? (size_t)p.R_max * 4 : 0);
     p.o_mxself = take(mx ? (size_t)p.R_max * 4 : 0);
+    p.o_mxt = take(mx ? (size_t)T * c.input_dim / 2 : 0);
+    p.o_mxts = take(mx ? mx_scales_bytes(L.mx, T, c.input_dim) : 0);
     p.o_mxx = take(mx ? (size_t)p.R_max * c.input_dim / 2 : 0);
     p.o_mxxs = take(mx ? mx_scales_bytes(L.mx, p.R_max, c.input_dim) : 0);
     p.o_mxh = take(mx ? (size_t)p.R_max * c.expert_dim / 2 : 0);
@@ -447,14 +450,13 @@ int64_t moe_capacity(const moe_layer_t *layer, int32_t T) {
 namespace {
 
 // Rows of bf16 `x` to the layer's 4-bit format, into the workspace.
-cudaError_t quantize_rows(moe_layer *L, const void *x, int x_rows, int cols, const int32_t *row_index, size_t o_codes,
+cudaError_t quantize_rows(moe_layer *L, const void *x, int rows, int cols, const int32_t *row_index, size_t o_codes,
                           size_t o_scales, cudaStream_t s) {
     MxQuantArgs a;
     a.x = x;
     a.ld = cols;
-    a.x_rows = x_rows;
+    a.x_rows = a.rows = rows;
     a.row_index = row_index;
-    a.rows = L->plan.R_max;
     a.cols = cols;
     a.pre = a.post = 1.f;
     a.codes = reinterpret_cast<uint8_t *>(L->ws + o_codes);
@@ -660,8 +662,19 @@ int fwd_route(moe_layer_t *L, const void *x, int32_t T, const float *logit_noise
         ma.token = reinterpret_cast<int32_t *>(ws + p.o_mxtok);
         ma.self = reinterpret_cast<int32_t *>(ws + p.o_mxself);
         MOE_LAUNCH(launch_mx_row_map(ma, s));
-        MOE_LAUNCH(quantize_rows(L, x, T, c.input_dim, ma.token, p.o_mxx, p.o_mxxs, s));
-        *nl += 2;
+        // Every token is quantised once and copied to its rows.
+        MOE_LAUNCH(quantize_rows(L, x, T, c.input_dim, nullptr, p.o_mxt, p.o_mxts, s));
+        MxGatherArgs ga;
+        ga.codes = reinterpret_cast<uint8_t *>(ws + p.o_mxt);
+        ga.scales = reinterpret_cast<uint8_t *>(ws + p.o_mxts);
+        ga.src_rows = T;
+        ga.rows = p.R_max;
+        ga.cols = c.input_dim;
+        ga.row_index = ma.token;
+        ga.out_codes = reinterpret_cast<uint8_t *>(ws + p.o_mxx);
+        ga.out_scales = reinterpret_cast<uint8_t *>(ws + p.o_mxxs);
+        MOE_LAUNCH(launch_mx_gather(ga, L->mx, s));
+        *nl += 3;
     } else if (L->tc) {
         ScatterArgs sa;
         sa.x = x;

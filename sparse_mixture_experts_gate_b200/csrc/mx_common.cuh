@@ -43,6 +43,16 @@ struct MxQuantArgs {
 };
 cudaError_t launch_mx_quantize(const MxQuantArgs &a, int format, bool bf16, int num_sms, cudaStream_t s);
 
+// Gathers quantised rows: output row r is row row_index[r] of the source (others
+// are skipped).
+struct MxGatherArgs {
+    const uint8_t *codes, *scales;  // src_rows x cols
+    int src_rows, rows, cols;
+    const int32_t *row_index;       // [rows]
+    uint8_t *out_codes, *out_scales;
+};
+cudaError_t launch_mx_gather(const MxGatherArgs &a, int format, cudaStream_t s);
+
 // Source rows for the rows of a layer's row space: `token` [rows] is the token of
 // each kept assignment's row and of each shared expert's row, `self` the row itself;
 // -1 for rows that hold nothing.

@@ -252,6 +252,32 @@ int moe_mx_quantize(int32_t format, const void *x, int32_t dtype, int64_t ld, in
     return launched(launch_mx_quantize(a, format, dtype == MOE_DTYPE_BF16, sms, as_stream(stream_v)), "moe_mx_quantize");
 }
 
+int moe_mx_gather(int32_t format, const void *codes, const void *scales, int32_t src_rows, int32_t cols,
+                  const int32_t *row_index, int32_t rows, void *out_codes, void *out_scales, void *stream_v) {
+    report_error(MOE_OK, "");
+    int rc = check_mx(format, rows, cols);
+    if (rc != MOE_OK) return rc;
+    if (src_rows < 0) return fail(MOE_ERR_INVALID_ARG, "src_rows must be >= 0 (got %d)", src_rows);
+    if (rows > 0 && (!row_index || !out_codes || !out_scales || (src_rows > 0 && (!codes || !scales))))
+        return fail(MOE_ERR_INVALID_ARG, "row_index, codes and scales are required when rows > 0");
+    if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(out_codes, 16) || !aligned(out_scales, 16))
+        return fail(MOE_ERR_INVALID_ARG, "codes and scales must be 16-byte aligned");
+    if (!aligned(row_index, 4)) return fail(MOE_ERR_INVALID_ARG, "row_index must be 4-byte aligned");
+    if (rows == 0 || src_rows == 0) return MOE_OK;
+    int sms = 0;
+    if ((rc = device_sms(&sms)) != MOE_OK) return rc;
+    MxGatherArgs a;
+    a.codes = static_cast<const uint8_t *>(codes);
+    a.scales = static_cast<const uint8_t *>(scales);
+    a.src_rows = src_rows;
+    a.rows = rows;
+    a.cols = cols;
+    a.row_index = row_index;
+    a.out_codes = static_cast<uint8_t *>(out_codes);
+    a.out_scales = static_cast<uint8_t *>(out_scales);
+    return launched(launch_mx_gather(a, format, as_stream(stream_v)), "moe_mx_gather");
+}
+
 int moe_mx_dequantize(int32_t format, const void *codes, const void *scales, int32_t rows, int32_t cols,
                       int32_t scale_exp, void *out, int32_t dtype, int64_t ld, void *stream_v) {
     report_error(MOE_OK, "");

@@ -2,7 +2,7 @@
 
 Routing to experts from given logits and its gradient (`route`, `route_backward`),
 and microscaled 4-bit floating point: rows of codes and scales (`MxTensor`), made by
-`mx_quantize`, read back by `mx_dequantize`, and multiplied with 4-bit expert
+`mx_quantize` (and `mx_gather`), read back by `mx_dequantize`, and multiplied with 4-bit expert
 weights by `mx_gemm`. Checks and pointer marshalling only; the work is done by the
 kernels behind the C ABI (include/moe.h has the definitions). Every call runs on the
 current stream of its tensors' device; nothing is differentiable through autograd.
@@ -162,6 +162,13 @@ def mx_tile_scales(scales: torch.Tensor) -> torch.Tensor:
     return p.view(G, nb, 4, 32, sb, 4).permute(0, 1, 4, 3, 2, 5).contiguous()
 
 
+def _empty_mx(fmt: str, rows: int, cols: int, scale_exp: int, device) -> MxTensor:
+    q = MxTensor.__new__(MxTensor)
+    q._set(fmt, _empty((rows, cols // 2), (cols // 2, 1), dtype=torch.uint8, device=device),
+           _empty((_scale_bytes(fmt, rows, cols),), (1,), dtype=torch.uint8, device=device), rows, cols, 1, scale_exp)
+    return q
+
+
 def mx_quantize(x: torch.Tensor, fmt: str = "mxfp4", row_index: Optional[torch.Tensor] = None, scale_exp: int = 0,
                 values: Optional[torch.Tensor] = None, out: Optional[MxTensor] = None) -> MxTensor:
     """Rows of x (bf16 or fp32) to 4 bits. row_index [rows] int32: output row r is x's row
@@ -177,21 +184,41 @@ def mx_quantize(x: torch.Tensor, fmt: str = "mxfp4", row_index: Optional[torch.T
         rows, index = x_rows, None
     else:
         rows, index = row_index.numel(), _array("row_index", row_index, x, torch.int32)
+    if out is None:
+        out = _empty_mx(fmt, rows, cols, scale_exp, x.device)
+    elif (out.format, out.rows, out.cols, out.groups, out.scale_exp) != (fmt, rows, cols, 1, scale_exp) or \
+            out.codes.device != x.device:
+        raise ValueError("out has another format, size, exponent or device")
+    if index is not None and values is None and rows >= 2 * x_rows and rows * cols >= 1 << 22:
+        # Rows that are wanted several times are quantised once and copied, where that is worth a launch.
+        q = mx_quantize(x, fmt, scale_exp=scale_exp)
+        _call(x.get_device(), "moe_mx_gather", B.lib().moe_mx_gather, B.MOE_MX[fmt], q.codes.data_ptr(),
+              q.scales.data_ptr(), x_rows, cols, index, rows, out.codes.data_ptr(), out.scales.data_ptr())
+        return out
     v = v_ld = 0
     if values is not None:
         if values.dtype != x.dtype or values.shape != (rows, cols) or values.device != x.device:
             raise ValueError(f"values: {x.dtype} {(rows, cols)} on {x.device} is needed")
         v, v_ld = values.data_ptr(), _rows("values", values)
-    if out is None:
-        codes = _empty((rows, cols // 2), (cols // 2, 1), dtype=torch.uint8, device=x.device)
-        scales = _empty((_scale_bytes(fmt, rows, cols),), (1,), dtype=torch.uint8, device=x.device)
-        out = MxTensor.__new__(MxTensor)
-        out._set(fmt, codes, scales, rows, cols, 1, scale_exp)
-    elif (out.format, out.rows, out.cols, out.groups, out.scale_exp) != (fmt, rows, cols, 1, scale_exp) or \
-            out.codes.device != x.device:
-        raise ValueError("out has another format, size, exponent or device")
     _call(x.get_device(), "moe_mx_quantize", B.lib().moe_mx_quantize, B.MOE_MX[fmt], x.data_ptr(), _DTYPE[x.dtype], ld,
           x_rows, cols, index, rows, scale_exp, out.codes.data_ptr(), out.scales.data_ptr(), v or None, v_ld)
+    return out
+
+
+def mx_gather(q: MxTensor, row_index: torch.Tensor, out: Optional[MxTensor] = None) -> MxTensor:
+    """Rows row_index [rows] (int32) of q; a row is left as it was in `out` where row_index is
+    no row of q."""
+    if q.groups != 1:
+        raise ValueError("one group at a time")
+    rows = row_index.numel()
+    index = _array("row_index", row_index, q.codes, torch.int32)
+    if out is None:
+        out = _empty_mx(q.format, rows, q.cols, q.scale_exp, q.codes.device)
+    elif (out.format, out.rows, out.cols, out.groups, out.scale_exp) != (q.format, rows, q.cols, 1, q.scale_exp) or \
+            out.codes.device != q.codes.device:
+        raise ValueError("out has another format, size, exponent or device")
+    _call(q.codes.get_device(), "moe_mx_gather", B.lib().moe_mx_gather, B.MOE_MX[q.format], q.codes.data_ptr(),
+          q.scales.data_ptr(), q.rows, q.cols, index, rows, out.codes.data_ptr(), out.scales.data_ptr())
     return out
 
 

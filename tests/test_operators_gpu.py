@@ -121,6 +121,27 @@ def test_quantize_gathers_rows_and_leaves_the_others():
         assert (ref.scale_bytes(q.scales, n, 160, fmt)[~live] == 0xCD).all()
 
 
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("rows,src,cols", [(1, 1, 32), (300, 70, 96), (513, 200, 2080), (5000, 9, 1408), (2100, 1000, 7168)])
+def test_gathered_rows_are_the_rows(fmt, rows, src, cols):
+    """Rows copied after quantisation, and quantised by index (which does so from a size on), with rows left out."""
+    g = gen(rows)
+    x = randn(g, src, cols).bfloat16()
+    index = torch.randint(-2, src + 2, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    live = (index >= 0) & (index < src)
+    c, b, _ = ref.quantize(x[index.clamp(0, src - 1).long()], fmt)
+    need = ops.B.moe_mx_scales_bytes(ops.B.MOE_MX[fmt], rows, cols)
+
+    def blank():
+        return ops.MxTensor(fmt, torch.full((rows, cols // 2), 0xAB, dtype=torch.uint8, device="cuda"),
+                            torch.full((need,), 0xCD, dtype=torch.uint8, device="cuda"), rows, cols)
+
+    for q in (ops.mx_gather(ops.mx_quantize(x, fmt), index, out=blank()), ops.mx_quantize(x, fmt, row_index=index, out=blank())):
+        assert torch.equal(ref.unpack(q.codes)[live], c[live]) and (q.codes[~live] == 0xAB).all()
+        s = ref.scale_bytes(q.scales, rows, cols, fmt)
+        assert torch.equal(s[live], b[live]) and (s[~live] == 0xCD).all()
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_quantize_strided_rows(dtype):
     """Row strides and starts that no vector load can take."""

@@ -77,6 +77,12 @@ def test_quantize_refusals(L):
         assert _quantize(L, **kw) == bad, kw
         assert B.moe_last_error()
     assert _quantize(L, rows=0, x_rows=0) == B.MOE_OK
+    ok = [0, P, P, 4, 64, P, 3, P, P, None]
+    for i, v in ((0, 7), (1, None), (2, P + 4), (3, -1), (4, 48), (5, None), (5, P + 2), (6, -1), (7, None), (7, P + 8), (8, None)):
+        a = list(ok)
+        a[i] = v
+        assert L.moe_mx_gather(*a) == bad, i
+    assert L.moe_mx_gather(0, None, None, 0, 64, P, 3, P, P, None) == B.MOE_OK
     assert L.moe_mx_dequantize(0, P, P, 3, 64, 0, None, 0, 64, None) == bad
     assert L.moe_mx_dequantize(0, P, P, 3, 64, 0, P, 0, 60, None) == bad
     assert L.moe_mx_dequantize(0, P + 4, P, 3, 64, 0, P, 0, 64, None) == bad

@@ -446,8 +446,7 @@ class MoELayer:
     def set_routing(self, cfg):
         """Route as an operators.RouteConfig says (moe_set_routing); None returns to
         the router's own selection."""
-        import torch
-        moe_set_routing(self.handle, None if cfg is None else cfg._c[torch.float32])
+        moe_set_routing(self.handle, None if cfg is None else cfg.struct)
 
     def prepare_experts_mx(self, fmt: Optional[str] = "mxfp4", w1_exp: Optional[int] = None,
                            w2_exp: Optional[int] = None, stream=None):

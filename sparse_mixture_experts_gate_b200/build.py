@@ -1,11 +1,13 @@
-"""Build libmoe.so (the C ABI of include/moe.h) for sm_100a with nvcc, in-tree.
+"""Build libmoe.so (the C ABI of include/moe.h) for sm_100a with nvcc, and _operators.so
+(the torch side of operators.py) with the host compiler, in-tree.
 
     python -m sparse_mixture_experts_gate_b200.build [--force]
 
 Each .cu under csrc/ is compiled to an object file with
 `-gencode arch=compute_100a,code=sm_100a -O3 -lineinfo`, in parallel, and linked
 into sparse_mixture_experts_gate_b200/libmoe.so with the CUDA runtime linked
-statically (the driver library is loaded at run time).
+statically (the driver library is loaded at run time). csrc/operators_torch.cpp is
+compiled against torch's headers and linked with libmoe.so beside it.
 """
 from __future__ import annotations
 
@@ -22,6 +24,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libmoe.so")
+OPERATORS_SRC = os.path.join(CSRC, "operators_torch.cpp")
+OPERATORS_PATH = os.path.join(PKG, "_operators.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -47,8 +51,37 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def build_operators(force: bool = False) -> str:
+    """_operators.so, after libmoe.so, which it is linked with."""
+    import sysconfig
+    import torch
+    deps = [OPERATORS_SRC, os.path.join(INCLUDE, "moe.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(OPERATORS_PATH) and \
+            all(os.path.getmtime(p) <= os.path.getmtime(OPERATORS_PATH) for p in deps):
+        return OPERATORS_PATH
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    headers = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        raise RuntimeError("no host C++ compiler found")
+    tmp = OPERATORS_PATH + f".tmp{os.getpid()}"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-shared", "-DTORCH_EXTENSION_NAME=_operators",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           *[a for h in headers for a in ("-isystem", h)], OPERATORS_SRC, "-o", tmp, "-L" + os.path.join(root, "lib"),
+           "-lc10", "-ltorch_cpu", "-ltorch_cuda", "-lc10_cuda", "-ltorch_python", "-L" + PKG, "-l:libmoe.so",
+           "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cxx} failed for {OPERATORS_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, OPERATORS_PATH)
+    return OPERATORS_PATH
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if not force and up_to_date():
+        build_operators()
         return LIB_PATH
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -73,6 +106,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    build_operators(force)
     return LIB_PATH
 
 

@@ -85,13 +85,13 @@ bool encode_bf16_store(CUtensorMap *m, const void *base, uint64_t inner, uint64_
 }  // namespace
 
 namespace moe {
-bool encode_mx_maps(MxMaps *m, int format, const void *a_codes, const void *a_scales, uint64_t rows, const void *w_codes,
+bool encode_mx_maps(MxMaps *m, bool narrow, int format, const void *a_codes, const void *a_scales, uint64_t rows, const void *w_codes,
                     const void *w_scales, uint64_t groups, int n, int k) {
     const int block = format == MOE_MX_MXFP4 ? 32 : 16;
     const uint64_t tiles = mx_scale_tiles(k, block);
     const uint32_t box = 256 / (4 * block);
     return encode_u8_2d(&m->w, w_codes, k / 2, groups * n, 128) && encode_u8_2d(&m->a, a_codes, k / 2, rows, 16) &&
-           encode_u8_2d(&m->a96, a_codes, k / 2, rows, 96) &&
+           (narrow || encode_u8_2d(&m->a96, a_codes, k / 2, rows, 96)) &&
            encode_scale_tiles(&m->sw, w_scales, tiles, groups * ((n + 127) / 128), box) &&
            encode_scale_tiles(&m->sa, a_scales, tiles, (rows + 127) / 128, box);
 }
@@ -737,7 +737,7 @@ int fwd_expert_gemms(moe_layer_t *L, cudaStream_t s, bool shared_only) {
             g.vec_ok = 1;
             g.status = status;
             MxMaps m;
-            if (!encode_mx_maps(&m, L->mx, xc[l], xs[l], p.R_max, L->mx_codes[l], L->mx_scales[l], E + S, out[l], in[l]))
+            if (!encode_mx_maps(&m, mx_gemm_narrow(g), L->mx, xc[l], xs[l], p.R_max, L->mx_codes[l], L->mx_scales[l], E + S, out[l], in[l]))
                 return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the 4-bit experts");
             MOE_LAUNCH(launch_mx_gemm(m, g, L->mx, L->num_sms, s));
             ++*nl;

@@ -92,7 +92,9 @@ struct MxGemmArgs {
 struct MxMaps {
     CUtensorMap w, a, a96, sw, sa;
 };
-bool encode_mx_maps(MxMaps *m, int format, const void *a_codes, const void *a_scales, uint64_t rows, const void *w_codes,
+// Whether a product runs in the form for short segments (which needs no 96-row map).
+bool mx_gemm_narrow(const MxGemmArgs &a);
+bool encode_mx_maps(MxMaps *m, bool narrow, int format, const void *a_codes, const void *a_scales, uint64_t rows, const void *w_codes,
                     const void *w_scales, uint64_t groups, int n, int k);
 cudaError_t launch_mx_gemm(const MxMaps &m, const MxGemmArgs &a, int format, int num_sms, cudaStream_t s);
 

@@ -562,10 +562,12 @@ cudaError_t launch_act(const MxMaps &m, const MxGemmArgs &a, int num_sms, cudaSt
 
 }  // namespace
 
+// Short segments: with few rows a group the narrow form is far ahead (128 experts, 1024 rows, K 4096,
+// N 1536: 81 us against 100).
+bool mx_gemm_narrow(const MxGemmArgs &a) { return a.filled <= (int64_t)64 * a.G; }
+
 cudaError_t launch_mx_gemm(const MxMaps &m, const MxGemmArgs &a, int format, int num_sms, cudaStream_t s) {
-    // Short segments: with few rows a group the narrow form is far ahead (128 experts, 1024 rows, K 4096,
-    // N 1536: 81 us against 100).
-    const bool narrow = a.filled <= (int64_t)64 * a.G;
+    const bool narrow = mx_gemm_narrow(a);
     // Both accumulators a unit from K = 4096 on: 223 us instead of 250 at K = 7168 (32 experts, 32768
     // rows, N 2048), where the epilogue is short beside the products; 123 instead of 113 at K = 2048
     // (64 experts, 49152 rows, N 1408).

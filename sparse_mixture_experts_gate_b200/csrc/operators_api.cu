@@ -338,9 +338,6 @@ int moe_mx_gemm(const moe_mx_gemm_t *p, void *stream_v) {
     if (p->rows == 0) return MOE_OK;
     int sms = 0;
     if ((rc = device_sms(&sms)) != MOE_OK) return rc;
-    MxMaps m;
-    if (!encode_mx_maps(&m, p->format, p->a_codes, p->a_scales, p->rows, p->w_codes, p->w_scales, p->groups, p->n, p->k))
-        return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the codes or scales");
     MxGemmArgs a;
     a.group_start = p->group_start;
     a.group_rows = p->group_rows;
@@ -359,6 +356,9 @@ int moe_mx_gemm(const moe_mx_gemm_t *p, void *stream_v) {
     a.status = p->status;
     // Rows beyond the 127 that each group's start may leave unused.
     a.filled = (int64_t)p->rows - (p->groups > 1 ? (int64_t)p->groups * 127 : 0);
+    MxMaps m;
+    if (!encode_mx_maps(&m, mx_gemm_narrow(a), p->format, p->a_codes, p->a_scales, p->rows, p->w_codes, p->w_scales, p->groups, p->n, p->k))
+        return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the codes or scales");
     return launched(launch_mx_gemm(m, a, p->format, sms, as_stream(stream_v)), "moe_mx_gemm");
 }
 

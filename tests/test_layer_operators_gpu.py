@@ -178,8 +178,10 @@ def test_layer_refusals():
         with pytest.raises(MoEError):
             layer.set_routing(cfg)
     c = ops.RouteConfig(8, 2)
+    c.struct.dtype = binding.MOE_DTYPE["bf16"]
     with pytest.raises(MoEError):
-        binding.moe_set_routing(layer.handle, c._c[torch.bfloat16])
+        layer.set_routing(c)
+    c.struct.dtype = binding.MOE_DTYPE["fp32"]
     n = binding.moe_experts_mx_bytes(layer.handle, 0)
     buf = torch.empty(n + 256, dtype=torch.uint8, device="cuda")
     s = torch.cuda.current_stream().cuda_stream

@@ -134,6 +134,18 @@ def test_python_refusals():
         ops.route(torch.zeros(2, 7), cfg)
     with pytest.raises(ValueError, match="contiguous"):
         ops.route(torch.zeros(8, 2).t(), cfg)
+    with pytest.raises(ValueError, match="out"):
+        ops.route(torch.zeros(2, 8), cfg, out=(torch.zeros(2, 2), None, None))
+    with pytest.raises(ValueError, match="bf16 or fp32"):
+        ops.route(torch.zeros(2, 8, dtype=torch.float16), cfg)
+    with pytest.raises(ValueError, match="bias"):
+        ops.route(torch.zeros(2, 8), cfg, bias=torch.zeros(7))
+    with pytest.raises(ValueError, match="row_index"):
+        ops.mx_quantize(torch.zeros(2, 64), row_index=torch.zeros(3, dtype=torch.int64))
+    with pytest.raises(ValueError, match="values"):
+        ops.mx_quantize(torch.zeros(2, 64), values=torch.zeros(2, 32))
+    with pytest.raises(ValueError, match="multiple of 32"):
+        ops.mx_quantize(torch.zeros(2, 40))
     with pytest.raises(ValueError, match="grad_weights"):
         ops.route_backward(torch.zeros(2, 3), torch.zeros(2, 8), torch.zeros(2, 2, dtype=torch.int32), cfg)
     with pytest.raises(ValueError, match="format"):

@@ -450,12 +450,13 @@ int64_t moe_capacity(const moe_layer_t *layer, int32_t T) {
 namespace {
 
 // Rows of bf16 `x` to the layer's 4-bit format, into the workspace.
-cudaError_t quantize_rows(moe_layer *L, const void *x, int rows, int cols, const int32_t *row_index, size_t o_codes,
-                          size_t o_scales, cudaStream_t s) {
+cudaError_t quantize_rows(moe_layer *L, const void *x, int x_rows, int rows, int cols, const int32_t *row_index,
+                          size_t o_codes, size_t o_scales, cudaStream_t s) {
     MxQuantArgs a;
     a.x = x;
     a.ld = cols;
-    a.x_rows = a.rows = rows;
+    a.x_rows = x_rows;
+    a.rows = rows;
     a.row_index = row_index;
     a.cols = cols;
     a.pre = a.post = 1.f;
@@ -662,19 +663,24 @@ int fwd_route(moe_layer_t *L, const void *x, int32_t T, const float *logit_noise
         ma.token = reinterpret_cast<int32_t *>(ws + p.o_mxtok);
         ma.self = reinterpret_cast<int32_t *>(ws + p.o_mxself);
         MOE_LAUNCH(launch_mx_row_map(ma, s));
-        // Every token is quantised once and copied to its rows.
-        MOE_LAUNCH(quantize_rows(L, x, T, c.input_dim, nullptr, p.o_mxt, p.o_mxts, s));
-        MxGatherArgs ga;
-        ga.codes = reinterpret_cast<uint8_t *>(ws + p.o_mxt);
-        ga.scales = reinterpret_cast<uint8_t *>(ws + p.o_mxts);
-        ga.src_rows = T;
-        ga.rows = p.R_max;
-        ga.cols = c.input_dim;
-        ga.row_index = ma.token;
-        ga.out_codes = reinterpret_cast<uint8_t *>(ws + p.o_mxx);
-        ga.out_scales = reinterpret_cast<uint8_t *>(ws + p.o_mxxs);
-        MOE_LAUNCH(launch_mx_gather(ga, L->mx, s));
-        *nl += 3;
+        // From 2^22 elements on every token is quantised once and copied to its rows; with fewer a launch costs more.
+        if ((int64_t)T * c.input_dim >= 1 << 22) {
+            MOE_LAUNCH(quantize_rows(L, x, T, T, c.input_dim, nullptr, p.o_mxt, p.o_mxts, s));
+            MxGatherArgs ga;
+            ga.codes = reinterpret_cast<uint8_t *>(ws + p.o_mxt);
+            ga.scales = reinterpret_cast<uint8_t *>(ws + p.o_mxts);
+            ga.src_rows = T;
+            ga.rows = p.R_max;
+            ga.cols = c.input_dim;
+            ga.row_index = ma.token;
+            ga.out_codes = reinterpret_cast<uint8_t *>(ws + p.o_mxx);
+            ga.out_scales = reinterpret_cast<uint8_t *>(ws + p.o_mxxs);
+            MOE_LAUNCH(launch_mx_gather(ga, L->mx, s));
+            ++*nl;
+        } else {
+            MOE_LAUNCH(quantize_rows(L, x, T, p.R_max, c.input_dim, ma.token, p.o_mxx, p.o_mxxs, s));
+        }
+        *nl += 2;
     } else if (L->tc) {
         ScatterArgs sa;
         sa.x = x;
@@ -715,7 +721,7 @@ int fwd_expert_gemms(moe_layer_t *L, cudaStream_t s, bool shared_only) {
         const int in[2] = {c.input_dim, c.expert_dim}, out[2] = {c.expert_dim, c.output_dim};
         for (int l = 0; l < 2; ++l) {
             if (l == 1) {
-                MOE_LAUNCH(quantize_rows(L, ws + p.o_h, p.R_max, c.expert_dim,
+                MOE_LAUNCH(quantize_rows(L, ws + p.o_h, p.R_max, p.R_max, c.expert_dim,
                                          reinterpret_cast<int32_t *>(ws + p.o_mxself), p.o_mxh, p.o_mxhs, s));
                 ++*nl;
             }

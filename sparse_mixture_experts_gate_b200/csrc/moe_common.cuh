@@ -469,6 +469,22 @@ __device__ __forceinline__ void spin_ns(uint64_t ns) {
     }
 }
 
+// ------------------------------------------------- programmatic dependent launch
+
+// Lets the stream's next kernel start (if it was launched to allow it) before this one has ended.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Waits until the stream's previous kernels have ended and their writes are visible.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// The launch attribute of a kernel that calls wait_for_previous before it touches global memory.
+inline cudaLaunchAttribute early_start_attribute() {
+    cudaLaunchAttribute a;
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
+    return a;
+}
+
 // ------------------------------------------------------------------ misc
 
 // Raises kernel K's dynamic shared-memory limit once per device (the first

@@ -178,6 +178,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_relinquish();
         }
     }
+    // All of this may run while the rows are still being quantised.
+    wait_for_previous();
     // Token tiles before each group: a scan over the groups, kThreads at a time.
     for (int g0 = 0, carry = 0; g0 < a.G; g0 += kThreads) {
         const int g = g0 + threadIdx.x;
@@ -539,13 +541,14 @@ cudaError_t launch(const MxMaps &m, const MxGemmArgs &a, int num_sms, cudaStream
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CG;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0] = early_start_attribute();
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CG == 2 ? 1 : 0;
+    cfg.numAttrs = CG == 2 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, mx_gemm_kernel<FMT, TILE, SUB, CG, ACT>, m, a);
 }
 

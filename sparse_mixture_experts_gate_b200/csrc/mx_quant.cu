@@ -228,6 +228,7 @@ __device__ __forceinline__ uint2 quantize16(const Raw<XT> &v, float pre, uint32_
 template <int FMT, typename XT, int STEPS, bool PRE>
 __global__ void __launch_bounds__(kThreads) mx_quantize_kernel(const MxQuantArgs a, int rpb, bool vec, bool vec_values) {
     constexpr int kWordLanes = MxFormat<FMT>::kTileK / kLaneElems;  // lanes of one word of 4 scales
+    launch_dependents();
     const int lane = threadIdx.x & 31;
     const int r0 = blockIdx.x * rpb;
     int src_l = -1;  // lane l: the source row of output row r0 + l
@@ -311,6 +312,8 @@ __global__ void __launch_bounds__(kThreads) mx_gather_kernel(const MxGatherArgs 
     const int lane = threadIdx.x & 31, warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     const int r0 = warp / 32 * 128 + warp % 32;
     if (r0 >= a.rows) return;
+    launch_dependents();
+    wait_for_previous();
     const int pieces = a.cols / 32;
     const int mine = lane < 4 && r0 + 32 * lane < a.rows ? a.row_index[r0 + 32 * lane] : -1;
     const uint4 *from[4];
@@ -374,9 +377,12 @@ bool vector_rows(const void *p, int64_t ld, int elem, int bytes) {
 template <int FMT, typename XT, int STEPS>
 cudaError_t quantize(const MxQuantArgs &a, int num_sms, cudaStream_t s) {
     const int64_t items = (int64_t)a.rows * ((a.cols + kStep * STEPS - 1) / (kStep * STEPS));
-    // Rows per block: one piece for each warp, and no more blocks than 64 for each SM.
+    // Rows per block: one piece for each warp, and no more blocks than 64 for each SM. An index far longer
+    // than x has mostly rows that are none: 8 rows a block (one token in 16256 rows x 4096 4 us, 6 with 4;
+    // 128 tokens in 17280, some blocks full, 8 us, 10 with 16).
     int rpb = 1;
     while (rpb < 32 && ((int64_t)rpb * items < (int64_t)a.rows * (kThreads / 32) || a.rows / rpb > 64 * num_sms)) rpb *= 2;
+    if (a.row_index && (int64_t)a.x_rows * 16 < a.rows) rpb = 8;
     const int blocks = (a.rows + rpb - 1) / rpb;
     const bool vec = vector_rows(a.x, a.ld, sizeof(XT), 32), vv = vector_rows(a.values, a.values_ld, sizeof(XT), 32);
     if (a.pre != 1.f) mx_quantize_kernel<FMT, XT, STEPS, true><<<blocks, kThreads, 0, s>>>(a, rpb, vec, vv);
@@ -402,8 +408,14 @@ cudaError_t launch_mx_quantize(const MxQuantArgs &a, int format, bool bf16, int 
 
 cudaError_t launch_mx_gather(const MxGatherArgs &a, int format, cudaStream_t s) {
     const int blocks = (a.rows - 1) / 128 * 4 + 4;  // 32 warps for every 128 rows
-    mx_gather_kernel<<<blocks, kThreads, 0, s>>>(a, mx_scale_tiles(a.cols, format == kMxFp4 ? 32 : 16));
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr = early_start_attribute();
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, mx_gather_kernel, a, mx_scale_tiles(a.cols, format == kMxFp4 ? 32 : 16));
 }
 
 cudaError_t launch_mx_row_map(const MxRowMapArgs &a, cudaStream_t s) {

@@ -163,8 +163,9 @@ py::tuple quantize(const Tensor &x, int format, const Maybe &row_index, int scal
     const Tensor scales = out_scales ? *out_scales : empty({scale_bytes(format, rows, cols)}, at::kByte, x);
     const int type = dtype_of("x", x.scalar_type());
     const int32_t n = count("rows", rows), nx = count("rows", x_rows), nc = count("columns", cols);
-    if (index && !values && rows >= 2 * x_rows && rows * cols >= 1 << 22) {
-        // Rows that are wanted several times are quantised once and copied, where that is worth a launch.
+    if (index && !values && rows >= 2 * x_rows && x_rows * cols >= 1 << 22) {
+        // Rows that are wanted several times are quantised once and copied, from a size on where that is worth
+        // the launch (many rows of the index may be none: the rows of x are what is sure).
         const Tensor c = empty({x_rows, cols / 2}, at::kByte, x);
         const Tensor s = empty({scale_bytes(format, x_rows, cols)}, at::kByte, x);
         check(moe_mx_quantize(format, x.data_ptr(), type, ld, nx, nc, nullptr, nx, scale_exp, c.data_ptr(), s.data_ptr(),

@@ -21,13 +21,14 @@
 //                of these (or two groups at the border of the selection) are closer
 //                together than their error: below 1% of the tokens for logits of
 //                variance 2 and 256 experts.
-// Bounds that route_fast relies on: above e^-16 of the largest possible one, a
-// sigmoid is off by 2^-19 of itself (__expf's 2 + 1.2 |l| ulp), and by 2^-21
-// absolutely; a softmax by 2^-19 of itself (the sum of at most 512 terms in 16 + 5
-// steps, expf, the division) and, but for the sum, which all keys share, by 2^-20.
-// So keys without a bias are in order if 2^-18 of themselves apart; with one the
-// error counts absolutely, 2^-18 of the largest score for two, and 2^-23 of the keys
-// for adding the biases. Logits themselves as keys are exact.
+// Bounds that route_fast relies on: a sigmoid is off by 2^-22 (__expf's 2 + 1.2 |l|
+// ulp times s (1 - s), and the reciprocal), and above e^-16 by 2^-19 of itself; a
+// softmax by 2^-19 of itself (the sum of at most 512 terms in 16 + 5 steps, expf, the
+// division) and, but for the sum, which all keys share, by 2^-20 down to e^-16 of the
+// largest. So keys without a bias are in order if 2^-18 of themselves apart; with one
+// the error counts absolutely, twice 2^-22 or 2^-19 of the largest score for two
+// keys, and 2^-23 of the keys for adding the biases; a group's score has two of them.
+// Logits themselves as keys are exact.
 //
 // What bounds it: the instructions, about 450 a token for 256 experts in 8 groups.
 #include <algorithm>
@@ -197,11 +198,20 @@ __device__ __forceinline__ int2 route_exact(const XT *src, double *row, const Ro
 #pragma unroll
         for (int q = 0; q < RE; ++q) code[q] = be == static_cast<uint32_t>(lane + 32 * q) ? 0ull : code[q];
     }
-    double s = 0.0;
-    if (choice >= 0) {
-        const double l = (double)logit(src, choice);
-        s = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)m) / z;
+    // The weights: in fp32 as route_fast's, unless they are too small for it.
+    const float l = choice >= 0 ? logit(src, choice) : -INFINITY, zf = static_cast<float>(z);
+    float sf = choice >= 0 ? (a.sigmoid ? __fdividef(1.f, 1.f + expf(-l)) : __fdividef(expf(l - m), zf)) : 0.f;
+    if (__all_sync(0xffffffffu, choice < 0 || sf > 0x1p-80f)) {
+        if (a.renormalize) {
+            float sum = sf;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            sf = sum > 0.f ? __fdividef(sf, sum) : 0.f;
+        }
+        return make_int2(choice, __float_as_int(sf * a.scale));
     }
+    double s = 0.0;
+    if (choice >= 0) s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)m) / z;
     if (a.renormalize) {
         const double sum = warp_sum(s);
         s = sum > 0.0 ? s / sum : 0.0;
@@ -292,6 +302,7 @@ __device__ __forceinline__ bool route_fast(float (&h)[RE], const float *bias, co
     }
     bool sure = true;
     const float smax = SIGMOID ? 1.f : z;  // no score is larger (a softmax's largest is exp(0) z)
+    const float apart = SIGMOID ? 0x1p-21f : 0x1p-18f * smax;  // what two scores may be off together
     if constexpr (by_logit) {
 #pragma unroll
         for (int q = 0; q < RE; ++q) key[q] = fmaxf(h[q] + 0.f, -INFINITY);  // one zero for both signs, NaN masked
@@ -326,9 +337,9 @@ __device__ __forceinline__ bool route_fast(float (&h)[RE], const float *bias, co
         const bool there = gr.g < a.groups, chosen = there && before < a.top_groups;
         const uint32_t lanes = __ballot_sync(0xffffffffu, chosen);
         if (a.top_groups < a.groups) {
-            // The lowest group inside against the highest one outside: two scores each, and the codes' 5 bits.
+            // The lowest group inside against the highest one outside.
             const float in = -warp_max(chosen ? -mine : -INFINITY), out = warp_max(there && !chosen ? mine : -INFINITY);
-            if (out != -INFINITY && !(in - out > 0x1p-17f * smax + 0x1p-22f * (fabsf(in) + fabsf(out)))) sure = false;
+            if (out != -INFINITY && !(in - out > 2.f * apart + 0x1p-22f * (fabsf(in) + fabsf(out)))) sure = false;
         }
 #pragma unroll
         for (int q = 0; q < RE; ++q)
@@ -377,8 +388,15 @@ __device__ __forceinline__ bool route_fast(float (&h)[RE], const float *bias, co
         v = choice >= 0 ? v : -INFINITY;
         float next = __shfl_down_sync(0xffffffffu, v, 1);
         if (lane == a.k - 1) next = left >= kNone ? code_key(left | kLow) : -INFINITY;
-        const float error = a.bias ? 0x1p-18f * smax + 0x1p-23f * fabsf(v) : 0x1p-18f * v;
-        const bool fine = lane >= a.k || next == -INFINITY || v - next > error;
+        const float error = a.bias ? apart + 0x1p-23f * fabsf(v) : 0x1p-18f * v;
+        bool fine = lane >= a.k || next == -INFINITY || v - next > error;
+        if (!__all_sync(0xffffffffu, fine || lane != a.k - 1)) {
+            // The first one left out may be as high as the lowest choice by its code: its whole key counts, if
+            // no other one has the same code.
+            const uint32_t rest = __reduce_max_sync(0xffffffffu, code[0] == left ? (RE > 1 ? code[1] : 0u) : code[0]);
+            if (lane == a.k - 1)
+                fine = (rest & ~kLow) < (left & ~kLow) && v - keys[padded(static_cast<int>(kLow - (left & kLow)))] > error;
+        }
         // Scores without a bias that are too small for the bounds are left to 64 bits.
         const bool small = !a.bias && choice >= 0 && !(v >= 0x1p-23f * smax);
         if (!__all_sync(0xffffffffu, fine && !small)) sure = false;

@@ -387,7 +387,8 @@ MOE_API int moe_ep_combine(moe_layer_t *layer, void *y, void *stream);
  * selection is the one of keys computed in 64 bits.
  * An expert whose logit is -inf or NaN, or whose key is, is never selected; where
  * fewer than num_active experts are left, the remaining choices have index -1 and
- * weight 0. A logit of +inf gives unspecified weights and valid indices. */
+ * weight 0. With a logit of +inf the token's weights are unspecified, and its indices
+ * are in range and different, or -1. */
 enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
 
 typedef struct {
@@ -468,7 +469,8 @@ MOE_API size_t moe_mx_scales_bytes(int32_t format, int64_t rows, int64_t cols);
  *   values     optional [rows] rows of cols, values_ld apart, in x's type: what
  *              codes and scales stand for (exact in both types, as long as it is in
  *              the type's range)
- * scale_exp in -60..60. Errors: INVALID_ARG, CUDA. */
+ * scale_exp in -60..60. Here and below rows are at most 2^31 - 1024 and cols 2^30.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 MOE_API int moe_mx_quantize(int32_t format, const void *x, int32_t dtype, int64_t ld, int32_t x_rows, int32_t cols,
                             const int32_t *row_index, int32_t rows, int32_t scale_exp, void *codes, void *scales,
                             void *values, int64_t values_ld, void *stream);
@@ -477,7 +479,7 @@ MOE_API int moe_mx_quantize(int32_t format, const void *x, int32_t dtype, int64_
  * row row_index[r] of codes and scales (src_rows x cols), and is left as it was
  * where that is outside 0..src_rows-1. The outputs may not overlap the inputs. With
  * rows that are wanted several times this costs less than quantising each of
- * them. Errors: INVALID_ARG, CUDA. */
+ * them. Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 MOE_API int moe_mx_gather(int32_t format, const void *codes, const void *scales, int32_t src_rows, int32_t cols,
                           const int32_t *row_index, int32_t rows, void *out_codes, void *out_scales, void *stream);
 
@@ -505,7 +507,8 @@ MOE_API int moe_mx_dequantize(int32_t format, const void *codes, const void *sca
  *   out                rows of n, out_ld apart, out_dtype MOE_DTYPE_*
  *   status             device word or NULL: bits are or-ed in (bit 0: a bounded
  *                      wait gave up, out is incomplete; bit 1 as above)
- * groups <= 1024, groups x n < 2^31. rows = 0 enqueues nothing. Needs no
+ * groups <= 1024, groups x n < 2^31 - 1024, and groups (rows / 192 + 1) n / 256 (short
+ * segments, rows < 192 groups: / 64 and / 128) below about 2^31. rows = 0 enqueues nothing. Needs no
  * workspace; calls on any streams may overlap. Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 typedef struct {
     int32_t format, rows, n, k, groups;

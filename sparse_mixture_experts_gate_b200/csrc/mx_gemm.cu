@@ -414,8 +414,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int u = first; u < total && ok; u += step, ++tcount) {
             const Unit w = unit_of(u);
             const int f0 = w.feat0 + static_cast<int>(rank) * kFeat + q * 32;
-            const float mul = a.post * (a.alpha ? __ldg(a.alpha + w.g) : 1.f);
-            auto bias_of = [&](int f) { return a.bias && f < a.N ? __ldg(a.bias + (int64_t)w.g * a.N + f) : 0.f; };
+            const float mul = a.post * (a.alpha ? a.alpha[w.g] : 1.f);
+            auto bias_of = [&](int f) { return a.bias && f < a.N ? a.bias[(int64_t)w.g * a.N + f] : 0.f; };
             float bv[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) bv[i] = bias_of(ACT == kActRuntime ? f0 + lane : f0 + lane / 4 + 8 * i);

@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kThreads) mx_gather_kernel(const MxGatherArgs 
     const int r0 = warp / 32 * 128 + warp % 32;
     if (r0 >= a.rows) return;
     launch_dependents();
-    wait_for_previous();
+    wait_for_previous();  // what is read below was written while this kernel lived: no read-only loads
     const int pieces = a.cols / 32;
     const int mine = lane < 4 && r0 + 32 * lane < a.rows ? a.row_index[r0 + 32 * lane] : -1;
     const uint4 *from[4];
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads) mx_gather_kernel(const MxGatherArgs 
         uint32_t w[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-            if (from[u]) w[u] = __ldg(reinterpret_cast<const uint32_t *>(sf[u] + (int64_t)j * 512));
+            if (from[u]) w[u] = *reinterpret_cast<const uint32_t *>(sf[u] + (int64_t)j * 512);
         uint32_t *to = reinterpret_cast<uint32_t *>(st + (int64_t)j * 512);
         if (all) {
             *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kThreads) mx_gather_kernel(const MxGatherArgs 
         uint4 v[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-            if (from[u]) v[u] = __ldg(from[u] + i);
+            if (from[u]) v[u] = from[u][i];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
             if (from[u]) to[(int64_t)(32 * u) * pieces + i] = v[u];

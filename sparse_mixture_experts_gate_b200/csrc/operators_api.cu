@@ -49,6 +49,11 @@ int device_sms(int *sms) {
 cudaStream_t as_stream(void *s) { return reinterpret_cast<cudaStream_t>(s); }
 bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
+bool overlap(const void *p, size_t np, const void *q, size_t nq) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return np && nq && a < b + nq && b < a + np;
+}
+
 int launched(cudaError_t e, const char *what) {
     return e == cudaSuccess ? MOE_OK : fail(MOE_ERR_CUDA, "%s failed: %s", what, cudaGetErrorString(e));
 }
@@ -112,9 +117,15 @@ int check_rows(const moe_route_config_t *c, const void *logits, int64_t ld, int3
     return MOE_OK;
 }
 
+// The kernels look up to a tile past a row or an element with 32-bit numbers.
+constexpr int kMxMaxRows = INT32_MAX - 1023, kMxMaxCols = 1 << 30;
+
 int check_mx(int format, int64_t rows, int64_t cols) {
     if (format != MOE_MX_MXFP4 && format != MOE_MX_NVFP4) return fail(MOE_ERR_INVALID_ARG, "unknown format %d", format);
     if (rows < 0) return fail(MOE_ERR_INVALID_ARG, "rows must be >= 0 (got %lld)", (long long)rows);
+    if (rows > kMxMaxRows || cols > kMxMaxCols)
+        return fail(MOE_ERR_UNSUPPORTED, "%lld rows of %lld elements: at most %d of %d are supported", (long long)rows,
+                    (long long)cols, kMxMaxRows, kMxMaxCols);
     if (cols < 32 || cols % 32)
         return fail(MOE_ERR_INVALID_ARG, "a row must have a positive multiple of 32 elements (got %lld)",
                     (long long)cols);
@@ -263,6 +274,10 @@ int moe_mx_gather(int32_t format, const void *codes, const void *scales, int32_t
     if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(out_codes, 16) || !aligned(out_scales, 16))
         return fail(MOE_ERR_INVALID_ARG, "codes and scales must be 16-byte aligned");
     if (!aligned(row_index, 4)) return fail(MOE_ERR_INVALID_ARG, "row_index must be 4-byte aligned");
+    const size_t row_bytes = cols / 2;
+    if (overlap(codes, src_rows * row_bytes, out_codes, rows * row_bytes) ||
+        overlap(scales, moe_mx_scales_bytes(format, src_rows, cols), out_scales, moe_mx_scales_bytes(format, rows, cols)))
+        return fail(MOE_ERR_INVALID_ARG, "the outputs may not overlap the inputs");
     if (rows == 0 || src_rows == 0) return MOE_OK;
     int sms = 0;
     if ((rc = device_sms(&sms)) != MOE_OK) return rc;
@@ -314,7 +329,7 @@ int moe_mx_gemm(const moe_mx_gemm_t *p, void *stream_v) {
     if (p->n < 1) return fail(MOE_ERR_INVALID_ARG, "n must be >= 1 (got %d)", p->n);
     if (p->groups < 1) return fail(MOE_ERR_INVALID_ARG, "groups must be >= 1 (got %d)", p->groups);
     if (p->groups > 1024) return fail(MOE_ERR_UNSUPPORTED, "groups > 1024 is not supported (got %d)", p->groups);
-    if ((int64_t)p->groups * p->n > INT32_MAX)
+    if ((int64_t)p->groups * p->n > INT32_MAX - 1023)
         return fail(MOE_ERR_UNSUPPORTED, "groups x n must be below 2^31");
     if ((p->group_start == nullptr) != (p->group_rows == nullptr))
         return fail(MOE_ERR_INVALID_ARG, "group_start and group_rows go together");
@@ -336,8 +351,6 @@ int moe_mx_gemm(const moe_mx_gemm_t *p, void *stream_v) {
         !aligned(p->status, 4))
         return fail(MOE_ERR_INVALID_ARG, "group_start, group_rows, bias, alpha and status must be 4-byte aligned");
     if (p->rows == 0) return MOE_OK;
-    int sms = 0;
-    if ((rc = device_sms(&sms)) != MOE_OK) return rc;
     MxGemmArgs a;
     a.group_start = p->group_start;
     a.group_rows = p->group_rows;
@@ -356,8 +369,15 @@ int moe_mx_gemm(const moe_mx_gemm_t *p, void *stream_v) {
     a.status = p->status;
     // Rows beyond the 127 that each group's start may leave unused.
     a.filled = (int64_t)p->rows - (p->groups > 1 ? (int64_t)p->groups * 127 : 0);
+    // Units are counted in 32 bits, even where (against the rule) every group claims all rows.
+    const bool narrow = mx_gemm_narrow(a);
+    const int64_t tiles = (int64_t)p->groups * (p->rows / (narrow ? 64 : 192) + 1);
+    if (tiles * ((p->n + 127) / (narrow ? 128 : 256) + 1) > INT32_MAX - 65535)
+        return fail(MOE_ERR_UNSUPPORTED, "%d rows x %d features in %d groups are too many", p->rows, p->n, p->groups);
+    int sms = 0;
+    if ((rc = device_sms(&sms)) != MOE_OK) return rc;
     MxMaps m;
-    if (!encode_mx_maps(&m, mx_gemm_narrow(a), p->format, p->a_codes, p->a_scales, p->rows, p->w_codes, p->w_scales, p->groups, p->n, p->k))
+    if (!encode_mx_maps(&m, narrow, p->format, p->a_codes, p->a_scales, p->rows, p->w_codes, p->w_scales, p->groups, p->n, p->k))
         return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the codes or scales");
     return launched(launch_mx_gemm(m, a, p->format, sms, as_stream(stream_v)), "moe_mx_gemm");
 }

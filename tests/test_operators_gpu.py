@@ -594,6 +594,84 @@ def test_captured_and_replayed_on_two_streams():
                 assert torch.equal(a, b)
 
 
+def test_replays_read_what_was_just_quantised():
+    """Rows quantised once, copied and multiplied, each kernel started while the one before it runs: a
+    graph replayed on changing inputs gives what separate calls give."""
+    g = gen(51)
+    cols, N, G = 4096, 256, 4
+    x = torch.empty(1100, cols, dtype=torch.bfloat16, device="cuda")
+    index = torch.randint(0, 1100, (4 * 640,), generator=g, device="cuda", dtype=torch.int32)
+    start = torch.arange(4, device="cuda", dtype=torch.int32) * 640
+    count = torch.tensor([640, 0, 513, 1], device="cuda", dtype=torch.int32)
+    _, w, _, _ = _operands(g, "nvfp4", 1, G, N, cols)
+    out = torch.zeros(4 * 640, N, dtype=torch.bfloat16, device="cuda")
+
+    def step():
+        return ops.mx_gemm(ops.mx_quantize(x, "nvfp4", row_index=index), w, start, count, out=out)
+
+    x.copy_(randn(g, 1100, cols))
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(20):
+        x.copy_(randn(g, 1100, cols))
+        index.copy_(torch.randint(0, 1100, (4 * 640,), generator=g, device="cuda"))
+        out.zero_()
+        graph.replay()
+        got = out.clone()
+        torch.cuda.synchronize()
+        q = ops.mx_quantize(x[index.long()], "nvfp4")
+        torch.cuda.synchronize()
+        want = ops.mx_gemm(q, w, start, count, out=torch.zeros_like(out))
+        assert torch.equal(got, want)
+
+
+# ------------------------------------------------------------------ offsets past 32 bits
+
+
+def _ends(n, m=300):
+    """The first and the last rows of n."""
+    return torch.cat([torch.arange(m), torch.arange(n - m, n)]).cuda()
+
+
+@pytest.mark.parametrize("E,score", [(256, "sigmoid"), (40, "softmax")])
+def test_route_of_many_tokens(E, score):
+    """More than 2^31 logits: the last tokens are routed as they are alone."""
+    T = 2 ** 31 // E + 12345
+    x = torch.empty(T, E, dtype=torch.bfloat16, device="cuda").normal_(generator=gen(60))
+    cfg = ops.RouteConfig(E, 2, score, renormalize=False)
+    w, idx, n = ops.route(x, cfg)
+    at = _ends(T)
+    lw, li, _ = ops.route(x[at], cfg)
+    assert torch.equal(idx[at], li) and torch.equal(w[at], lw)
+    assert torch.equal(n.long(), torch.bincount(idx.reshape(-1), minlength=E))
+    d = ops.route_backward(w, x, idx, cfg, out=torch.full_like(x, 7))
+    assert torch.equal(d[at], ops.route_backward(w[at], x[at], idx[at], cfg))
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_rows_and_products_past_32_bits(fmt):
+    """More than 2^31 elements of x, 2^31 bytes of codes and 2^31 outputs."""
+    g = gen(61)
+    rows, cols = 2 ** 31 // 14336 + 40, 28672
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    at = _ends(rows)
+    q, few = ops.mx_quantize(x, fmt), ops.mx_quantize(x[at], fmt)
+    del x
+    back = ops.mx_gather(q, at.to(torch.int32))
+    assert torch.equal(back.codes, few.codes)
+    assert torch.equal(ref.scale_bytes(back.scales, 600, cols, fmt), ref.scale_bytes(few.scales, 600, cols, fmt))
+    assert torch.equal(ops.mx_dequantize(q, torch.bfloat16)[at], ops.mx_dequantize(few, torch.bfloat16))
+    _, w, _, _ = _operands(g, fmt, 1, 1, 100, cols)
+    assert torch.equal(ops.mx_gemm(q, w)[at], ops.mx_gemm(few, w))
+    rows = 2 ** 31 // 640 + 77
+    x = torch.empty(rows, 32, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    at = _ends(rows)
+    _, w, _, _ = _operands(g, fmt, 1, 1, 640, 32)
+    assert torch.equal(ops.mx_gemm(ops.mx_quantize(x, fmt), w)[at], ops.mx_gemm(ops.mx_quantize(x[at], fmt), w))
+
+
 def test_errors_reach_python():
     with pytest.raises(MoEError):
         ops.route(torch.zeros(2, 6, device="cuda"), ops.RouteConfig(6, 2, num_groups=4))

@@ -168,3 +168,23 @@ def test_reference_rounds_as_the_formats_say():
     assert ref.quantize(u * 1.3, "mxfp4")[2][0, 7] == 6.0
     _, byte, v = ref.quantize(torch.full((1, 32), 6.0 * 17, dtype=torch.float64), "nvfp4")
     assert v[0, 0] == 6.0 * 16  # 17 lies between the scales 16 and 18: the even one
+
+
+def test_sizes_that_32_bits_do_not_hold(L):
+    no, top = B.MOE_ERR_UNSUPPORTED, 2 ** 31 - 1
+    assert _quantize(L, x_rows=top, rows=top) == no and _quantize(L, cols=2 ** 30 + 32, ld=2 ** 31) == no
+    assert L.moe_mx_gather(0, P, P, 4, 64, P, top, P, P, None) == no
+    assert L.moe_mx_dequantize(0, P, P, top, 64, 0, P, 0, 64, None) == no
+    g = dict(format=0, k=64, scale_exp=0, activation=-1, out_dtype=0, a_codes=P, a_scales=P, w_codes=P, w_scales=P,
+             group_start=P, group_rows=P, bias=None, alpha=None, out=P, status=None)
+    for size in (dict(rows=top, n=8, groups=1), dict(rows=2 ** 28, n=1024, groups=512), dict(rows=2 ** 30, n=2 ** 18, groups=1),
+                 dict(rows=4, n=2 ** 21, groups=1023 + 1)):
+        a = B.MoeMxGemm(**g, **size, out_ld=size["n"])
+        assert L.moe_mx_gemm(ctypes.byref(a), None) == no, size
+
+
+def test_gather_refuses_its_own_rows(L):
+    bad, n = B.MOE_ERR_INVALID_ARG, 1 << 20
+    assert L.moe_mx_gather(0, P, P + n, 8, 64, P, 8, P, P + 2 * n, None) == bad
+    assert L.moe_mx_gather(0, P, P + n, 8, 64, P, 8, P + 16, P + 2 * n, None) == bad
+    assert L.moe_mx_gather(0, P, P + n, 8, 64, P, 300, P + 2 * n, P + n - 512, None) == bad

@@ -116,8 +116,8 @@ __device__ __forceinline__ int staged(int r, int p) { return r * 64 + ((p ^ (r >
 // Arrives on an mbarrier of either CTA of the pair with CTA-scope release. What
 // it hands over is the accumulator, whose loads have completed (wait::ld, then the
 // tcgen05 fence); a cluster-scope release would also wait for this thread's
-// earlier output stores to land (with it, 147 instead of 103 us for 64 experts,
-// 49152 rows, 1408 x 2048, NVFP4, swish).
+// earlier output stores to land (with it, 147 instead of 131 us for 64 experts,
+// 49152 rows, 1408 x 2048, NVFP4, swish, when this was changed).
 __device__ __forceinline__ void arrive_pair(uint32_t bar_cluster_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster_addr) : "memory");
 }
@@ -565,15 +565,15 @@ cudaError_t launch_act(const MxMaps &m, const MxGemmArgs &a, int num_sms, cudaSt
 
 }  // namespace
 
-// Short segments: with few rows a group the narrow form is far ahead (128 experts, 1024 rows, K 4096,
-// N 1536: 81 us against 100).
+// Short segments: with few rows a group the narrow form is ahead (128 experts, 1024 rows, K 4096, N 1536:
+// 81 us against 95).
 bool mx_gemm_narrow(const MxGemmArgs &a) { return a.filled <= (int64_t)64 * a.G; }
 
 cudaError_t launch_mx_gemm(const MxMaps &m, const MxGemmArgs &a, int format, int num_sms, cudaStream_t s) {
     const bool narrow = mx_gemm_narrow(a);
-    // Both accumulators a unit from K = 4096 on: 223 us instead of 250 at K = 7168 (32 experts, 32768
-    // rows, N 2048), where the epilogue is short beside the products; 123 instead of 113 at K = 2048
-    // (64 experts, 49152 rows, N 1408).
+    // Both accumulators a unit from K = 4096 on: 218 us instead of 251 at K = 7168 (32 experts, 32768
+    // rows, N 2048, MXFP4), where the epilogue is short beside the products; 123 instead of 113 at K = 2048
+    // (64 experts, 49152 rows, N 1408, NVFP4).
     const bool deep = a.K >= 4096;
     if (format == kMxFp4)
         return narrow ? launch_act<kMxFp4, 64, 1, 1>(m, a, num_sms, s)

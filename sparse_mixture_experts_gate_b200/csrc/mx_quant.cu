@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads) mx_dequantize_kernel(const MxDequant
 // Rows of codes and scales to other rows. A warp takes rows i, i + 32, i + 64 and
 // i + 96 of 128: their pieces are in flight together, and their words of a scale tile
 // are 16 neighbouring bytes. Where a token goes to several experts, quantising it
-// once and copying it costs less than quantising each row (8192 tokens x 2048 to 49152 rows, NVFP4: 31 us against 49).
+// once and copying it costs less than quantising each row (8192 tokens x 2048 to 49152 rows, NVFP4: 31 us against 47).
 __global__ void __launch_bounds__(kThreads) mx_gather_kernel(const MxGatherArgs a, int SB) {
     const int lane = threadIdx.x & 31, warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     const int r0 = warp / 32 * 128 + warp % 32;

@@ -4,7 +4,7 @@
 // Argument checks, output tensors and the calls of the C ABI (include/moe.h), on
 // the current stream of the tensors' device. For a call on a few tokens the host's
 // work is what counts: the same through Python and ctypes took 12 us for the routing
-// of one token, and takes 6 us here, 3 of them the launch.
+// of one token, and takes 5 us here, 3 of them the launch.
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
@@ -163,9 +163,11 @@ py::tuple quantize(const Tensor &x, int format, const Maybe &row_index, int scal
     const Tensor scales = out_scales ? *out_scales : empty({scale_bytes(format, rows, cols)}, at::kByte, x);
     const int type = dtype_of("x", x.scalar_type());
     const int32_t n = count("rows", rows), nx = count("rows", x_rows), nc = count("columns", cols);
-    if (index && !values && rows >= 2 * x_rows && x_rows * cols >= 1 << 22) {
-        // Rows that are wanted several times are quantised once and copied, from a size on where that is worth
-        // the launch (many rows of the index may be none: the rows of x are what is sure).
+    if (index && !values && rows >= 3 * x_rows && x_rows * cols >= 1 << 22) {
+        // Rows that are wanted several times are quantised once and copied: 8192 x 2048 NVFP4 to six times as many
+        // rows 31 us, 47 without; to twice as many it is no gain (32768 x 7168: 223 and 213). Below this size it
+        // is not worth the launch (2048 x 2048 to 12288 rows 12 and 15, 1024 x 2048 to 6144 11 and 10). Many
+        // rows of the index may be none: the rows of x are what is sure.
         const Tensor c = empty({x_rows, cols / 2}, at::kByte, x);
         const Tensor s = empty({scale_bytes(format, x_rows, cols)}, at::kByte, x);
         check(moe_mx_quantize(format, x.data_ptr(), type, ld, nx, nc, nullptr, nx, scale_exp, c.data_ptr(), s.data_ptr(),

@@ -19,8 +19,8 @@
 //                highest value that the first one left out can have;
 //   route_exact  does it in 64 bits, for the tokens whose fp32 keys do not tell, as two
 //                of these (or two groups at the border of the selection) are closer
-//                together than their error: below 1% of the tokens for logits of
-//                variance 2 and 256 experts.
+//                together than their error: 0.1% to 0.5% of the tokens for normal
+//                logits and 256 experts.
 // Bounds that route_fast relies on: a sigmoid is off by 2^-22 (__expf's 2 + 1.2 |l|
 // ulp times s (1 - s), and the reciprocal), and above e^-16 by 2^-19 of itself; a
 // softmax by 2^-19 of itself (the sum of at most 512 terms in 16 + 5 steps, expf, the
@@ -30,7 +30,9 @@
 // keys, and 2^-23 of the keys for adding the biases; a group's score has two of them.
 // Logits themselves as keys are exact.
 //
-// What bounds it: the instructions, about 450 a token for 256 experts in 8 groups.
+// What bounds it: the instructions, about 850 a token for 256 experts in 8 groups,
+// 8 selected, sigmoids and a bias (32768 tokens: 43 us, the issue slots 67% taken and the
+// ALU 60%, where reading the logits takes 7; 17 us for one expert of 256 by its logit).
 #include <algorithm>
 #include <type_traits>
 
@@ -43,7 +45,6 @@ namespace {
 constexpr int kThreads = 256;   // of the forward
 constexpr int kWarps = kThreads / 32;
 constexpr int kUndecided = 256;  // undecided tokens that a block puts by
-constexpr int kMaxCluster = 8;  // blocks that put their counts together without atomics
 constexpr int kBackThreads = 256;
 constexpr int kBackWarps = kBackThreads / 32;
 
@@ -417,16 +418,10 @@ __device__ __forceinline__ bool route_fast(float (&h)[RE], const float *bias, co
     return true;
 }
 
-__device__ __forceinline__ int ld_shared_cluster(uint32_t addr) {
-    int v;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
-
-// cluster: the whole grid is one cluster, whose blocks add their counts up among
-// themselves; otherwise they are added to `counts` (zeroed before) by atomics.
+// A grid of one block writes its counts; the blocks of a larger one add theirs to `counts`
+// (zeroed before) by atomics.
 template <typename XT, int RE, int MODE, bool SIGMOID>
-__global__ void __launch_bounds__(kThreads, RE > 8 ? 2 : 3) route_kernel(const __grid_constant__ RouteArgs a, bool cluster) {
+__global__ void __launch_bounds__(kThreads, RE > 8 ? 2 : 3) route_kernel(const __grid_constant__ RouteArgs a) {
     __shared__ int32_t hist[kRouteMaxExperts];
     __shared__ __align__(8) float rows[kWarps][(32 + kPad) * RE];  // logits and keys, or a row of 64-bit keys
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -505,18 +500,9 @@ __global__ void __launch_bounds__(kThreads, RE > 8 ? 2 : 3) route_kernel(const _
         if (threadIdx.x == 0) n_undecided = 0;
     } while (__syncthreads_or(token(i) < a.T));
     if (!a.counts) return;
-    if (cluster) {
-        cluster_sync_all();
-        for (int e = blockIdx.x + gridDim.x * threadIdx.x; e < a.E; e += gridDim.x * kThreads) {
-            int n = 0;
-            for (uint32_t b = 0; b < gridDim.x; ++b) n += ld_shared_cluster(mapa_shared(smem_u32(&hist[e]), b));
-            a.counts[e] = n;
-        }
-        cluster_sync_all();  // no block leaves while others read its counts
-    } else {
-        __syncthreads();
-        for (int e = threadIdx.x; e < a.E; e += kThreads)
-            if (hist[e]) atomicAdd(a.counts + e, hist[e]);
+    for (int e = threadIdx.x; e < a.E; e += kThreads) {
+        if (gridDim.x == 1) a.counts[e] = hist[e];
+        else if (hist[e]) atomicAdd(a.counts + e, hist[e]);
     }
 }
 
@@ -634,31 +620,16 @@ __global__ void __launch_bounds__(kBackThreads) route_backward_kernel(const __gr
 template <typename XT, int RE, int MODE, bool SIGMOID>
 cudaError_t launch_forward(const RouteArgs &a, int num_sms, cudaStream_t s) {
     const int64_t blocks = ((int64_t)a.T + kWarps - 1) / kWarps;
-    // Up to four tokens a warp of one cluster: no zeroing of the counts before (2 us of host time and a
-    // launch less; 128 tokens: 4 against 6 us on the device).
-    const bool cluster = a.counts && blocks <= 4 * kMaxCluster;
-    int n = 1;
-    if (cluster) {
-        while (n < kMaxCluster && n < blocks) n *= 2;
-    } else {
-        if (a.counts) {
-            const cudaError_t e = cudaMemsetAsync(a.counts, 0, sizeof(int32_t) * a.E, s);
-            if (e != cudaSuccess) return e;
-        }
-        n = static_cast<int>(std::min<int64_t>(blocks, (int64_t)num_sms * (RE > 8 ? 2 : 3)));
+    const int n = static_cast<int>(std::min<int64_t>(blocks, (int64_t)num_sms * (RE > 8 ? 2 : 3)));
+    // One block needs no zeroed counts: a call every 5.2 us, 6.1 with the memset. (A cluster of up to 8 blocks
+    // could add its counts up without it too: a call every 5.6 us, but its result comes 0.7 us later for 64
+    // tokens and 1 to 3 us later for 128 and more.)
+    if (a.counts && n > 1) {
+        const cudaError_t e = cudaMemsetAsync(a.counts, 0, sizeof(int32_t) * a.E, s);
+        if (e != cudaSuccess) return e;
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(n, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = n;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = cluster ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, route_kernel<XT, RE, MODE, SIGMOID>, a, cluster);
+    route_kernel<XT, RE, MODE, SIGMOID><<<n, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
 }
 
 template <typename XT, int RE>

@@ -130,7 +130,7 @@ def mx_experts(layer, inp, out, fmt, exps):
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
-@pytest.mark.parametrize("name,T,kw", [("default", 1000, {}), ("e64", 700, {}), ("e64", 1, {}), ("decode", 128, {}),
+@pytest.mark.parametrize("name,T,kw", [("default", 1000, {}), ("e64", 700, {}), ("e64", 1, {}), ("decode", 128, {}), ("e64", 2100, {}),
                                        ("default", 260, dict(S=2, capacity_factor=0.3, activation="relu")),
                                        ("e64", 150, dict(capacity_factor=0.0, credit_norm="hidden")),
                                        ("default", 300, dict(E=1, k=1, capacity_factor=0.0))])

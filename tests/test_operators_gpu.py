@@ -122,7 +122,8 @@ def test_quantize_gathers_rows_and_leaves_the_others():
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
-@pytest.mark.parametrize("rows,src,cols", [(1, 1, 32), (300, 70, 96), (513, 200, 2080), (5000, 9, 1408), (2100, 1000, 7168)])
+@pytest.mark.parametrize("rows,src,cols", [(1, 1, 32), (300, 70, 96), (513, 200, 2080), (5000, 9, 1408), (2100, 1000, 7168),
+                                           (3100, 1000, 7168)])
 def test_gathered_rows_are_the_rows(fmt, rows, src, cols):
     """Rows copied after quantisation, and quantised by index (which does so from a size on), with rows left out."""
     g = gen(rows)
@@ -600,11 +601,11 @@ def test_replays_read_what_was_just_quantised():
     g = gen(51)
     cols, N, G = 4096, 256, 4
     x = torch.empty(1100, cols, dtype=torch.bfloat16, device="cuda")
-    index = torch.randint(0, 1100, (4 * 640,), generator=g, device="cuda", dtype=torch.int32)
-    start = torch.arange(4, device="cuda", dtype=torch.int32) * 640
+    index = torch.randint(0, 1100, (4 * 896,), generator=g, device="cuda", dtype=torch.int32)
+    start = torch.arange(4, device="cuda", dtype=torch.int32) * 896
     count = torch.tensor([640, 0, 513, 1], device="cuda", dtype=torch.int32)
     _, w, _, _ = _operands(g, "nvfp4", 1, G, N, cols)
-    out = torch.zeros(4 * 640, N, dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros(4 * 896, N, dtype=torch.bfloat16, device="cuda")
 
     def step():
         return ops.mx_gemm(ops.mx_quantize(x, "nvfp4", row_index=index), w, start, count, out=out)
@@ -616,7 +617,7 @@ def test_replays_read_what_was_just_quantised():
         step()
     for _ in range(20):
         x.copy_(randn(g, 1100, cols))
-        index.copy_(torch.randint(0, 1100, (4 * 640,), generator=g, device="cuda"))
+        index.copy_(torch.randint(0, 1100, (4 * 896,), generator=g, device="cuda"))
         out.zero_()
         graph.replay()
         got = out.clone()

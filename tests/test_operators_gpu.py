@@ -447,6 +447,27 @@ def test_product_of_groups(fmt, act, bias, alpha, rows, N, K, extra):
         assert (out[~live] == 77).all()
 
 
+@pytest.mark.parametrize("fmt,G,N,K", [("mxfp4", 1024, 40, 96), ("nvfp4", 577, 33, 288), ("mxfp4", 90, 264, 4096),
+                                       ("nvfp4", 17, 520, 4128)])
+def test_product_of_many_groups(fmt, G, N, K):
+    """Segments of every size around a tile's, in the forms for long ones: each row is there once."""
+    g = gen(G)
+    sizes = torch.tensor([0, 1, 31, 32, 33, 100, 191, 192, 193, 300, 383, 384, 385, 400], device="cuda")
+    rows = sizes[torch.randint(0, 14, (G,), generator=g, device="cuda")].tolist()
+    start, n, R = _plan(rows)
+    exps = (0, 0) if fmt == "mxfp4" else (1, -4)
+    a, w, av, wv = _operands(g, fmt, R, G, N, K, exps)
+    out = torch.full((R, N), 77.0, dtype=torch.bfloat16, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ops.mx_gemm(a, w, start, n, out=out, status=st)
+    assert st.item() == 0
+    live = torch.zeros(R, dtype=torch.bool, device="cuda")
+    for e, (s, r) in enumerate(zip(start.tolist(), rows)):
+        live[s:s + r] = True
+        _check_product(out[s:s + r], av[s:s + r] @ wv[e].T, av[s:s + r].abs() @ wv[e].abs().T, K, None, True)
+    assert (out[~live] == 77).all()
+
+
 def test_product_of_extreme_scales():
     """Scales from one end of each format to the other: the sum is right where fp32 holds it."""
     for fmt, lo, hi in (("mxfp4", 100, 150), ("nvfp4", 1, 126)):

@@ -30,8 +30,8 @@
 // keys, and 2^-23 of the keys for adding the biases; a group's score has two of them.
 // Logits themselves as keys are exact.
 //
-// What bounds it: the instructions, about 850 a token for 256 experts in 8 groups,
-// 8 selected, sigmoids and a bias (32768 tokens: 43 us, the issue slots 67% taken and the
+// What bounds it: the instructions, about 800 a token for 256 experts in 8 groups,
+// 8 selected, sigmoids and a bias (32768 tokens: 41 us, the issue slots 67% taken and the
 // ALU 60%, where reading the logits takes 7; 17 us for one expert of 256 by its logit).
 #include <algorithm>
 #include <type_traits>
@@ -64,11 +64,12 @@ __device__ __forceinline__ float logit(const XT *src, int e) {
 
 // What a lane needs to know of the groups, once for all tokens: `width` lanes (a power
 // of two) look at each group of experts, this one at those of group g from base on,
-// below `end`, `width` apart; every lane takes `steps` steps. bit[q]: the first lane
-// of expert lane + 32 q's group.
+// below `end`, `width` apart; every lane takes `steps` steps, which are all inside one group and 32 experts where
+// `even`. bit[q]: the first lane of expert lane + 32 q's group.
 template <int RE>
 struct Groups {
     int width, g, steps, base, end;
+    bool even;
     uint32_t bit[RE];
 
     __device__ __forceinline__ Groups(const RouteArgs &a, int lane) {
@@ -78,6 +79,7 @@ struct Groups {
         steps = (gs + width - 1) / width;
         base = g * gs + lane % width;
         end = min(g + 1, a.groups) * gs;
+        even = a.groups * width == 32 && 32 % gs == 0 && gs % width == 0;
 #pragma unroll
         for (int q = 0; q < RE; ++q) bit[q] = 1u << min((lane + 32 * q) / gs, a.groups - 1) * width;
     }
@@ -319,11 +321,17 @@ __device__ __forceinline__ bool route_fast(float (&h)[RE], const float *bias, co
     }
     if constexpr (MODE == kGrouped) {
         float t1 = -INFINITY, t2 = -INFINITY;
-#pragma unroll 4
-        for (int j = 0, e = gr.base; j < gr.steps; ++j, e += gr.width) {
-            const float v = e < gr.end ? keys[padded(e)] : -INFINITY;
+        auto take = [&](float v) {
             t2 = fmaxf(t2, fminf(t1, v));
             t1 = fmaxf(t1, v);
+        };
+        if (gr.even) {
+            const float *p = keys + padded(gr.base);
+#pragma unroll 4
+            for (int j = 0; j < gr.steps; ++j, p += gr.width) take(*p);
+        } else {
+#pragma unroll 4
+            for (int j = 0, e = gr.base; j < gr.steps; ++j, e += gr.width) take(e < gr.end ? keys[padded(e)] : -INFINITY);
         }
         __syncwarp();
         for (int off = 1; off < gr.width; off <<= 1)
@@ -332,9 +340,12 @@ __device__ __forceinline__ bool route_fast(float (&h)[RE], const float *bias, co
         // Scores with the group's index in the lowest bits: the check below sees to those that this puts out
         // of order.
         const uint32_t rank = (key_code(mine) & ~31u) | (31u - gr.g);
+        // Each of a group's lanes compares with every width-th group.
         int before = 0;
-#pragma unroll 4
-        for (int o = 0; o < a.groups; ++o) before += __shfl_sync(0xffffffffu, rank, o * gr.width) > rank;
+#pragma unroll 2
+        for (int o = lane & (gr.width - 1), left = a.groups; left > 0; left -= gr.width, o += gr.width)
+            before += __shfl_sync(0xffffffffu, rank, o * gr.width) > rank && o < a.groups;
+        for (int off = 1; off < gr.width; off <<= 1) before += __shfl_xor_sync(0xffffffffu, before, off);
         const bool there = gr.g < a.groups, chosen = there && before < a.top_groups;
         const uint32_t lanes = __ballot_sync(0xffffffffu, chosen);
         if (a.top_groups < a.groups) {

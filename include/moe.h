@@ -475,6 +475,15 @@ MOE_API int moe_mx_quantize(int32_t format, const void *x, int32_t dtype, int64_
                             const int32_t *row_index, int32_t rows, int32_t scale_exp, void *codes, void *scales,
                             void *values, int64_t values_ld, void *stream);
 
+/* moe_mx_quantize with a row_index (and without values) in another way: quantises every row of x once, into
+ * `workspace` (>= moe_mx_once_bytes(format, x_rows, cols) bytes, 16-byte aligned), and copies the result to the
+ * rows that want it. The same outputs; less work where rows are wanted three times or more.
+ * Errors: as there, and WORKSPACE. */
+MOE_API size_t moe_mx_once_bytes(int32_t format, int64_t x_rows, int64_t cols);
+MOE_API int moe_mx_quantize_once(int32_t format, const void *x, int32_t dtype, int64_t ld, int32_t x_rows, int32_t cols,
+                                 const int32_t *row_index, int32_t rows, int32_t scale_exp, void *codes, void *scales,
+                                 void *workspace, size_t ws_bytes, void *stream);
+
 /* Gathers quantised rows: row r of out_codes and out_scales (rows x cols) becomes
  * row row_index[r] of codes and scales (src_rows x cols), and is left as it was
  * where that is outside 0..src_rows-1. The outputs may not overlap the inputs. With

@@ -31,7 +31,7 @@ EXPORTS = ("moe_config_default", "moe_layer_create", "moe_workspace_bytes", "moe
            "moe_selftest_router_timeout", "moe_router_planes_bytes", "moe_prepare_router",
            "moe_ep_dispatch", "moe_ep_layout", "moe_ep_experts_workspace_bytes", "moe_ep_experts", "moe_ep_combine", "moe_device_status", "moe_set_timing_events", "moe_launch_count", "moe_destroy", "moe_status_string",
            "moe_last_error", "moe_route_config_default", "moe_route", "moe_route_backward", "moe_mx_codes_bytes",
-           "moe_mx_scales_bytes", "moe_mx_quantize", "moe_mx_gather", "moe_mx_dequantize", "moe_mx_gemm", "moe_set_routing",
+           "moe_mx_scales_bytes", "moe_mx_quantize", "moe_mx_once_bytes", "moe_mx_quantize_once", "moe_mx_gather", "moe_mx_dequantize", "moe_mx_gemm", "moe_set_routing",
            "moe_experts_mx_bytes", "moe_prepare_experts_mx")
 
 
@@ -162,6 +162,10 @@ def lib() -> ctypes.CDLL:
         L.moe_mx_scales_bytes.argtypes = [i32, i64, i64]
         L.moe_mx_quantize.restype = ctypes.c_int
         L.moe_mx_quantize.argtypes = [i32, vp, i32, i64, i32, i32, vp, i32, i32, vp, vp, vp, i64, vp]
+        L.moe_mx_once_bytes.restype = sz
+        L.moe_mx_once_bytes.argtypes = [i32, i64, i64]
+        L.moe_mx_quantize_once.restype = ctypes.c_int
+        L.moe_mx_quantize_once.argtypes = [i32, vp, i32, i64, i32, i32, vp, i32, i32, vp, vp, vp, sz, vp]
         L.moe_mx_gather.restype = ctypes.c_int
         L.moe_mx_gather.argtypes = [i32, vp, vp, i32, i32, vp, i32, vp, vp, vp]
         L.moe_mx_dequantize.restype = ctypes.c_int
@@ -320,6 +324,17 @@ def moe_mx_quantize(fmt: int, x: Optional[int], dtype: int, ld: int, x_rows: int
                     values_ld: int, stream: int) -> int:
     return _check(lib().moe_mx_quantize(fmt, x, dtype, ld, x_rows, cols, row_index, rows, scale_exp, codes, scales,
                                         values, values_ld, stream), "moe_mx_quantize")
+
+
+def moe_mx_once_bytes(fmt: int, x_rows: int, cols: int) -> int:
+    return int(lib().moe_mx_once_bytes(fmt, x_rows, cols))
+
+
+def moe_mx_quantize_once(fmt: int, x: Optional[int], dtype: int, ld: int, x_rows: int, cols: int,
+                         row_index: Optional[int], rows: int, scale_exp: int, codes: Optional[int],
+                         scales: Optional[int], workspace: Optional[int], ws_bytes: int, stream: int) -> int:
+    return _check(lib().moe_mx_quantize_once(fmt, x, dtype, ld, x_rows, cols, row_index, rows, scale_exp, codes, scales,
+                                             workspace, ws_bytes, stream), "moe_mx_quantize_once")
 
 
 def moe_mx_gather(fmt: int, codes: Optional[int], scales: Optional[int], src_rows: int, cols: int,

@@ -451,8 +451,9 @@ namespace {
 
 // Rows of bf16 `x` to the layer's 4-bit format, into the workspace.
 cudaError_t quantize_rows(moe_layer *L, const void *x, int x_rows, int rows, int cols, const int32_t *row_index,
-                          size_t o_codes, size_t o_scales, cudaStream_t s) {
+                          size_t o_codes, size_t o_scales, cudaStream_t s, bool plain = false) {
     MxQuantArgs a;
+    a.plain = plain;
     a.x = x;
     a.ld = cols;
     a.x_rows = x_rows;
@@ -666,8 +667,9 @@ int fwd_route(moe_layer_t *L, const void *x, int32_t T, const float *logit_noise
         // Where a token has three rows or more, and from 2^22 elements on, it is quantised once and copied to
         // them; otherwise that costs more (mx_quantize's figures in operators_torch.cpp).
         if (k + S >= 3 && (int64_t)T * c.input_dim >= 1 << 22) {
-            MOE_LAUNCH(quantize_rows(L, x, T, T, c.input_dim, nullptr, p.o_mxt, p.o_mxts, s));
+            MOE_LAUNCH(quantize_rows(L, x, T, T, c.input_dim, nullptr, p.o_mxt, p.o_mxts, s, true));
             MxGatherArgs ga;
+            ga.plain = true;
             ga.codes = reinterpret_cast<uint8_t *>(ws + p.o_mxt);
             ga.scales = reinterpret_cast<uint8_t *>(ws + p.o_mxts);
             ga.src_rows = T;

@@ -36,7 +36,8 @@ struct MxQuantArgs {
     int rows, cols;
     float pre;                 // 2^-scale_exp
     uint8_t *codes;            // [rows][cols / 2]
-    uint8_t *scales;           // tiles
+    uint8_t *scales;           // tiles, or where `plain` rows of 4 SB bytes (for a gather that reads them)
+    bool plain = false;
     void *values;              // [rows][values_ld] in x's type, or null
     int64_t values_ld;
     float post;                // 2^scale_exp
@@ -46,7 +47,8 @@ cudaError_t launch_mx_quantize(const MxQuantArgs &a, int format, bool bf16, int 
 // Gathers quantised rows: output row r is row row_index[r] of the source (others
 // are skipped).
 struct MxGatherArgs {
-    const uint8_t *codes, *scales;  // src_rows x cols
+    const uint8_t *codes, *scales;  // src_rows x cols; scales in tiles, or where `plain` rows of 4 SB bytes
+    bool plain = false;
     int src_rows, rows, cols;
     const int32_t *row_index;       // [rows]
     uint8_t *out_codes, *out_scales;

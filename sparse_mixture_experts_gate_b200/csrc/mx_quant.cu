@@ -251,7 +251,9 @@ __global__ void __launch_bounds__(kThreads) mx_quantize_kernel(const MxQuantArgs
         }
         uint8_t *codes = a.codes + (int64_t)r * (a.cols / 2) + c0 / 2;
         const int j = c0 / MxFormat<FMT>::kTileK;  // scale tile of this lane's block
-        uint8_t *tile = a.scales + ((int64_t)(r / 128) * SB + j) * 512 + (r % 32) * 16 + (r % 128 / 32) * 4;
+        uint8_t *tile = a.scales + (a.plain ? ((int64_t)r * SB + j) * 4
+                                            : ((int64_t)(r / 128) * SB + j) * 512 + (r % 32) * 16 + (r % 128 / 32) * 4);
+        const int tile_bytes = a.plain ? 4 : 512;
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
             const int c = c0 + kStep * s;
@@ -264,7 +266,7 @@ __global__ void __launch_bounds__(kThreads) mx_quantize_kernel(const MxQuantArgs
 #pragma unroll
             for (int off = kBlockLanes; off < kWordLanes; off <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, off);
             if (lane % kWordLanes == 0 && j + kStep / MxFormat<FMT>::kTileK * s < SB)
-                *reinterpret_cast<uint32_t *>(tile + kStep / MxFormat<FMT>::kTileK * 512 * s) = word;
+                *reinterpret_cast<uint32_t *>(tile + kStep / MxFormat<FMT>::kTileK * s * tile_bytes) = word;
             if (c < a.cols) {
                 *reinterpret_cast<uint2 *>(codes + kStep / 2 * s) = code;
                 if (a.values) {
@@ -308,6 +310,10 @@ __global__ void __launch_bounds__(kThreads) mx_dequantize_kernel(const MxDequant
 // i + 96 of 128: their pieces are in flight together, and their words of a scale tile
 // are 16 neighbouring bytes. Where a token goes to several experts, quantising it
 // once and copying it costs less than quantising each row (8192 tokens x 2048 to 49152 rows, NVFP4: 31 us against 47).
+//
+// A row's scales in tiles are words of 4 bytes 512 bytes apart, each a 32-byte sector to read: where the codes were
+// made for this copy their scales lie row by row (PLAIN).
+template <bool PLAIN>
 __global__ void __launch_bounds__(kThreads) mx_gather_kernel(const MxGatherArgs a, int SB) {
     const int lane = threadIdx.x & 31, warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     const int r0 = warp / 32 * 128 + warp % 32;
@@ -324,7 +330,7 @@ __global__ void __launch_bounds__(kThreads) mx_gather_kernel(const MxGatherArgs 
         const int src = __shfl_sync(0xffffffffu, mine, u);
         const bool live = src >= 0 && src < a.src_rows;
         from[u] = live ? reinterpret_cast<const uint4 *>(a.codes + (int64_t)src * (a.cols / 2)) : nullptr;
-        sf[u] = a.scales + (int64_t)(src / 128) * SB * 512 + (src % 32) * 16 + (src % 128 / 32) * 4;
+        sf[u] = a.scales + (PLAIN ? (int64_t)src * SB * 4 : (int64_t)(src / 128) * SB * 512 + (src % 32) * 16 + (src % 128 / 32) * 4);
         all = all && live;
     }
     uint8_t *st = a.out_scales + (int64_t)(r0 / 128) * SB * 512 + (r0 % 32) * 16;
@@ -332,7 +338,7 @@ __global__ void __launch_bounds__(kThreads) mx_gather_kernel(const MxGatherArgs 
         uint32_t w[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-            if (from[u]) w[u] = *reinterpret_cast<const uint32_t *>(sf[u] + (int64_t)j * 512);
+            if (from[u]) w[u] = *reinterpret_cast<const uint32_t *>(sf[u] + (int64_t)j * (PLAIN ? 4 : 512));
         uint32_t *to = reinterpret_cast<uint32_t *>(st + (int64_t)j * 512);
         if (all) {
             *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -415,7 +421,8 @@ cudaError_t launch_mx_gather(const MxGatherArgs &a, int format, cudaStream_t s) 
     cudaLaunchAttribute attr = early_start_attribute();
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, mx_gather_kernel, a, mx_scale_tiles(a.cols, format == kMxFp4 ? 32 : 16));
+    return cudaLaunchKernelEx(&cfg, a.plain ? mx_gather_kernel<true> : mx_gather_kernel<false>, a,
+                              mx_scale_tiles(a.cols, format == kMxFp4 ? 32 : 16));
 }
 
 cudaError_t launch_mx_row_map(const MxRowMapArgs &a, cudaStream_t s) {

@@ -1,6 +1,7 @@
 // operators_api.cu - the C ABI of the operators that need no layer: routing
 // from given logits (moe_route, moe_route_backward) and microscaled 4-bit rows
 // and products (moe_mx_*). Argument checks, tensor maps, launches.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -138,6 +139,38 @@ int check_exp(int e) {
 
 int block_of(int format) { return format == MOE_MX_MXFP4 ? 32 : 16; }
 
+// Checks a quantisation's arguments and fills the kernel's.
+int quantize_args(MxQuantArgs *a, int32_t format, const void *x, int32_t dtype, int64_t ld, int32_t x_rows, int32_t cols,
+                  const int32_t *row_index, int32_t rows, int32_t scale_exp, void *codes, void *scales) {
+    int rc = check_mx(format, rows, cols);
+    if (rc != MOE_OK) return rc;
+    if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_FP32) return fail(MOE_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+    if (x_rows < 0) return fail(MOE_ERR_INVALID_ARG, "x_rows must be >= 0 (got %d)", x_rows);
+    if (!row_index && rows != x_rows)
+        return fail(MOE_ERR_INVALID_ARG, "without row_index, rows (%d) must equal x_rows (%d)", rows, x_rows);
+    if (ld < cols) return fail(MOE_ERR_INVALID_ARG, "x: row stride below cols");
+    if ((rc = check_exp(scale_exp)) != MOE_OK) return rc;
+    if (rows > 0 && ((!x && x_rows > 0) || !codes || !scales))
+        return fail(MOE_ERR_INVALID_ARG, "x, codes and scales (or the workspace) are required when rows > 0");
+    if (!aligned(x, dtype == MOE_DTYPE_BF16 ? 2 : 4) || !aligned(row_index, 4))
+        return fail(MOE_ERR_INVALID_ARG, "x and row_index must be aligned to their elements");
+    if (!aligned(codes, 16) || !aligned(scales, 16))
+        return fail(MOE_ERR_INVALID_ARG, "codes, scales and the workspace must be 16-byte aligned");
+    a->x = x;
+    a->ld = ld;
+    a->x_rows = x_rows;
+    a->row_index = row_index;
+    a->rows = rows;
+    a->cols = cols;
+    a->pre = std::ldexp(1.f, -scale_exp);
+    a->codes = static_cast<uint8_t *>(codes);
+    a->scales = static_cast<uint8_t *>(scales);
+    a->values = nullptr;
+    a->values_ld = 0;
+    a->post = std::ldexp(1.f, scale_exp);
+    return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -228,39 +261,58 @@ int moe_mx_quantize(int32_t format, const void *x, int32_t dtype, int64_t ld, in
                     const int32_t *row_index, int32_t rows, int32_t scale_exp, void *codes, void *scales, void *values,
                     int64_t values_ld, void *stream_v) {
     report_error(MOE_OK, "");
-    int rc = check_mx(format, rows, cols);
+    MxQuantArgs a;
+    int rc = quantize_args(&a, format, x, dtype, ld, x_rows, cols, row_index, rows, scale_exp, codes, scales);
     if (rc != MOE_OK) return rc;
-    if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_FP32) return fail(MOE_ERR_INVALID_ARG, "unknown dtype %d", dtype);
-    const size_t es = dtype == MOE_DTYPE_BF16 ? 2 : 4;
-    if (x_rows < 0) return fail(MOE_ERR_INVALID_ARG, "x_rows must be >= 0 (got %d)", x_rows);
-    if (!row_index && rows != x_rows)
-        return fail(MOE_ERR_INVALID_ARG, "without row_index, rows (%d) must equal x_rows (%d)", rows, x_rows);
-    if (ld < cols) return fail(MOE_ERR_INVALID_ARG, "x: row stride below cols");
     if (values && values_ld < cols) return fail(MOE_ERR_INVALID_ARG, "values: row stride below cols");
-    if ((rc = check_exp(scale_exp)) != MOE_OK) return rc;
-    if (rows > 0 && ((!x && x_rows > 0) || !codes || !scales))
-        return fail(MOE_ERR_INVALID_ARG, "x, codes and scales are required when rows > 0");
-    if (!aligned(x, es) || !aligned(values, es) || !aligned(row_index, 4))
-        return fail(MOE_ERR_INVALID_ARG, "x, values and row_index must be aligned to their elements");
-    if (!aligned(codes, 16) || !aligned(scales, 16))
-        return fail(MOE_ERR_INVALID_ARG, "codes and scales must be 16-byte aligned");
+    if (!aligned(values, dtype == MOE_DTYPE_BF16 ? 2 : 4))
+        return fail(MOE_ERR_INVALID_ARG, "values must be aligned to its elements");
     if (rows == 0 || x_rows == 0) return MOE_OK;
     int sms = 0;
     if ((rc = device_sms(&sms)) != MOE_OK) return rc;
-    MxQuantArgs a;
-    a.x = x;
-    a.ld = ld;
-    a.x_rows = x_rows;
-    a.row_index = row_index;
-    a.rows = rows;
-    a.cols = cols;
-    a.pre = std::ldexp(1.f, -scale_exp);
-    a.codes = static_cast<uint8_t *>(codes);
-    a.scales = static_cast<uint8_t *>(scales);
     a.values = values;
     a.values_ld = values_ld;
-    a.post = std::ldexp(1.f, scale_exp);
     return launched(launch_mx_quantize(a, format, dtype == MOE_DTYPE_BF16, sms, as_stream(stream_v)), "moe_mx_quantize");
+}
+
+size_t moe_mx_once_bytes(int32_t format, int64_t x_rows, int64_t cols) {
+    if ((format != MOE_MX_MXFP4 && format != MOE_MX_NVFP4) || x_rows < 0 || cols < 32 || cols % 32) return 0;
+    return (size_t)x_rows * (cols / 2 + 4 * mx_scale_tiles(static_cast<int>(std::min<int64_t>(cols, kMxMaxCols)), block_of(format)));
+}
+
+int moe_mx_quantize_once(int32_t format, const void *x, int32_t dtype, int64_t ld, int32_t x_rows, int32_t cols,
+                         const int32_t *row_index, int32_t rows, int32_t scale_exp, void *codes, void *scales,
+                         void *workspace, size_t ws_bytes, void *stream_v) {
+    report_error(MOE_OK, "");
+    MxQuantArgs a;
+    int rc = quantize_args(&a, format, x, dtype, ld, x_rows, cols, nullptr, x_rows, scale_exp, workspace, workspace);
+    if (rc != MOE_OK || (rc = check_mx(format, rows, cols)) != MOE_OK) return rc;
+    if (rows > 0 && (!row_index || !codes || !scales))
+        return fail(MOE_ERR_INVALID_ARG, "row_index, codes and scales are required when rows > 0");
+    if (!aligned(row_index, 4)) return fail(MOE_ERR_INVALID_ARG, "row_index must be 4-byte aligned");
+    if (!aligned(codes, 16) || !aligned(scales, 16))
+        return fail(MOE_ERR_INVALID_ARG, "codes and scales must be 16-byte aligned");
+    if (ws_bytes < moe_mx_once_bytes(format, x_rows, cols))
+        return fail(MOE_ERR_WORKSPACE, "workspace: %zu bytes given, %zu needed", ws_bytes,
+                    moe_mx_once_bytes(format, x_rows, cols));
+    if (rows == 0 || x_rows == 0) return MOE_OK;
+    int sms = 0;
+    if ((rc = device_sms(&sms)) != MOE_OK) return rc;
+    a.scales = a.codes + (size_t)x_rows * (cols / 2);
+    a.plain = true;
+    rc = launched(launch_mx_quantize(a, format, dtype == MOE_DTYPE_BF16, sms, as_stream(stream_v)), "moe_mx_quantize_once");
+    if (rc != MOE_OK) return rc;
+    MxGatherArgs g;
+    g.codes = a.codes;
+    g.scales = a.scales;
+    g.plain = true;
+    g.src_rows = x_rows;
+    g.rows = rows;
+    g.cols = cols;
+    g.row_index = row_index;
+    g.out_codes = static_cast<uint8_t *>(codes);
+    g.out_scales = static_cast<uint8_t *>(scales);
+    return launched(launch_mx_gather(g, format, as_stream(stream_v)), "moe_mx_quantize_once");
 }
 
 int moe_mx_gather(int32_t format, const void *codes, const void *scales, int32_t src_rows, int32_t cols,

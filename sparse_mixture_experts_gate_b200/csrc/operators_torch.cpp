@@ -168,14 +168,11 @@ py::tuple quantize(const Tensor &x, int format, const Maybe &row_index, int scal
         // rows 31 us, 47 without; to twice as many it is no gain (32768 x 7168: 223 and 213). Below this size it
         // is not worth the launch (2048 x 2048 to 12288 rows 12 and 15, 1024 x 2048 to 6144 11 and 10). Many
         // rows of the index may be none: the rows of x are what is sure.
-        const Tensor c = empty({x_rows, cols / 2}, at::kByte, x);
-        const Tensor s = empty({scale_bytes(format, x_rows, cols)}, at::kByte, x);
-        check(moe_mx_quantize(format, x.data_ptr(), type, ld, nx, nc, nullptr, nx, scale_exp, c.data_ptr(), s.data_ptr(),
-                              nullptr, 0, on.stream),
-              "moe_mx_quantize");
-        check(moe_mx_gather(format, c.data_ptr(), s.data_ptr(), nx, nc, index, n, codes.data_ptr(), scales.data_ptr(),
-                            on.stream),
-              "moe_mx_gather");
+        const int64_t bytes = static_cast<int64_t>(moe_mx_once_bytes(format, x_rows, cols));
+        const Tensor workspace = empty({bytes}, at::kByte, x);
+        check(moe_mx_quantize_once(format, x.data_ptr(), type, ld, nx, nc, index, n, scale_exp, codes.data_ptr(),
+                                   scales.data_ptr(), workspace.data_ptr(), bytes, on.stream),
+              "moe_mx_quantize_once");
     } else {
         check(moe_mx_quantize(format, x.data_ptr(), type, ld, nx, nc, index, n, scale_exp, codes.data_ptr(),
                               scales.data_ptr(), values ? values->data_ptr() : nullptr,

@@ -143,6 +143,36 @@ def test_gathered_rows_are_the_rows(fmt, rows, src, cols):
         assert torch.equal(s[live], b[live]) and (s[~live] == 0xCD).all()
 
 
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,src,cols,exp", [(1, 1, 32, 0), (7, 3, 96, -4), (700, 130, 160, 3), (513, 200, 2080, 0), (90, 257, 4128, 0)])
+def test_quantize_once_is_quantize(fmt, dtype, rows, src, cols, exp):
+    """Rows quantised once and copied, through the C ABI and its workspace, and rows that are none left alone."""
+    g = gen(rows + cols)
+    x = randn(g, src, cols + 5).to(dtype)[:, 3:cols + 3]
+    index = torch.randint(-1, src + 1, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    f, B = ops.B.MOE_MX[fmt], ops.B
+    need, ws = B.moe_mx_scales_bytes(f, rows, cols), B.moe_mx_once_bytes(f, src, cols)
+    got = []
+    for once in (True, False):
+        codes = torch.full((rows, cols // 2), 0xAB, dtype=torch.uint8, device="cuda")
+        scales = torch.full((need,), 0xCD, dtype=torch.uint8, device="cuda")
+        space = torch.full((ws + 16,), 0x5A, dtype=torch.uint8, device="cuda")
+        head = (f, x.data_ptr(), B.MOE_DTYPE["bf16" if dtype is torch.bfloat16 else "fp32"], cols + 5, src, cols,
+                index.data_ptr(), rows, exp, codes.data_ptr(), scales.data_ptr())
+        s = torch.cuda.current_stream().cuda_stream
+        if once:
+            B.moe_mx_quantize_once(*head, space.data_ptr(), ws, s)
+            assert (space[ws:] == 0x5A).all()
+        else:
+            B.moe_mx_quantize(*head, None, 0, s)
+        got.append((codes, scales))
+    assert torch.equal(got[0][0], got[1][0])
+    a, b = (ref.scale_bytes(s, rows, cols, fmt) for _, s in got)
+    live = (index >= 0) & (index < src)
+    assert torch.equal(a, b) and (a[~live] == 0xCD).all() and (got[0][0][~live] == 0xAB).all()
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_quantize_strided_rows(dtype):
     """Row strides and starts that no vector load can take."""

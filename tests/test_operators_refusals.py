@@ -90,6 +90,21 @@ def test_quantize_refusals(L):
     assert L.moe_mx_dequantize(1, P, P, 0, 64, 0, None, 0, 64, None) == B.MOE_OK
 
 
+def test_quantize_once_refusals(L):
+    ok = dict(fmt=0, x=P, dtype=0, ld=64, x_rows=3, cols=64, index=P, rows=9, exp=0, codes=P, scales=P, ws=P, n=3 * 36)
+    for change, code in ((dict(fmt=2), B.MOE_ERR_INVALID_ARG), (dict(x=None), B.MOE_ERR_INVALID_ARG), (dict(ld=63), B.MOE_ERR_INVALID_ARG),
+                         (dict(dtype=2), B.MOE_ERR_INVALID_ARG), (dict(cols=48), B.MOE_ERR_INVALID_ARG),
+                         (dict(index=None), B.MOE_ERR_INVALID_ARG), (dict(index=P + 2), B.MOE_ERR_INVALID_ARG),
+                         (dict(rows=-1), B.MOE_ERR_INVALID_ARG), (dict(x_rows=-1), B.MOE_ERR_INVALID_ARG),
+                         (dict(codes=None), B.MOE_ERR_INVALID_ARG), (dict(scales=P + 8), B.MOE_ERR_INVALID_ARG),
+                         (dict(ws=None), B.MOE_ERR_INVALID_ARG), (dict(ws=P + 8), B.MOE_ERR_INVALID_ARG),
+                         (dict(n=3 * 36 - 1), B.MOE_ERR_WORKSPACE), (dict(exp=61), B.MOE_ERR_INVALID_ARG),
+                         (dict(rows=2 ** 31 - 1), B.MOE_ERR_UNSUPPORTED), (dict(rows=0), B.MOE_OK)):
+        assert L.moe_mx_quantize_once(*{**ok, **change}.values(), None) == code, change
+    assert B.moe_mx_once_bytes(0, 3, 64) == 3 * 36 and B.moe_mx_once_bytes(1, 5, 96) == 5 * (48 + 8)
+    assert B.moe_mx_once_bytes(2, 3, 64) == 0 and B.moe_mx_once_bytes(0, -1, 64) == 0 and B.moe_mx_once_bytes(0, 3, 40) == 0
+
+
 def test_sizes(L):
     assert B.moe_mx_codes_bytes(3, 64) == 96 and B.moe_mx_codes_bytes(3, 40) == 0 and B.moe_mx_codes_bytes(-1, 64) == 0
     assert B.moe_mx_scales_bytes(0, 1, 128) == 512 and B.moe_mx_scales_bytes(0, 129, 160) == 2048

@@ -664,9 +664,9 @@ int fwd_route(moe_layer_t *L, const void *x, int32_t T, const float *logit_noise
         ma.token = reinterpret_cast<int32_t *>(ws + p.o_mxtok);
         ma.self = reinterpret_cast<int32_t *>(ws + p.o_mxself);
         MOE_LAUNCH(launch_mx_row_map(ma, s));
-        // Where a token has three rows or more, and from 2^22 elements on, it is quantised once and copied to
+        // Where a token has three rows or more, and from 2^21 elements on, it is quantised once and copied to
         // them; otherwise that costs more (mx_quantize's figures in operators_torch.cpp).
-        if (k + S >= 3 && (int64_t)T * c.input_dim >= 1 << 22) {
+        if (k + S >= 3 && (int64_t)T * c.input_dim >= 1 << 21) {
             MOE_LAUNCH(quantize_rows(L, x, T, T, c.input_dim, nullptr, p.o_mxt, p.o_mxts, s, true));
             MxGatherArgs ga;
             ga.plain = true;

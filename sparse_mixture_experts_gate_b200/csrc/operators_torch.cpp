@@ -163,11 +163,11 @@ py::tuple quantize(const Tensor &x, int format, const Maybe &row_index, int scal
     const Tensor scales = out_scales ? *out_scales : empty({scale_bytes(format, rows, cols)}, at::kByte, x);
     const int type = dtype_of("x", x.scalar_type());
     const int32_t n = count("rows", rows), nx = count("rows", x_rows), nc = count("columns", cols);
-    if (index && !values && rows >= 3 * x_rows && x_rows * cols >= 1 << 22) {
+    if (index && !values && rows >= 3 * x_rows && x_rows * cols >= 1 << 21) {
         // Rows that are wanted several times are quantised once and copied: 8192 x 2048 NVFP4 to six times as many
-        // rows 31 us, 47 without; to twice as many it is no gain (32768 x 7168: 223 and 213). Below this size it
-        // is not worth the launch (2048 x 2048 to 12288 rows 12 and 15, 1024 x 2048 to 6144 11 and 10). Many
-        // rows of the index may be none: the rows of x are what is sure.
+        // rows 27 us, 49 without, 32768 x 7168 MXFP4 to three times 210 and 254; to twice as many it is little or no
+        // gain (170 and 172). Below this size it is not worth the launch (1024 x 2048 to 6144 rows 8 and 10 us, 256 x
+        // 7168 to 2048 12 and 10). Many rows of the index may be none: the rows of x are what is sure.
         const int64_t bytes = static_cast<int64_t>(moe_mx_once_bytes(format, x_rows, cols));
         const Tensor workspace = empty({bytes}, at::kByte, x);
         check(moe_mx_quantize_once(format, x.data_ptr(), type, ld, nx, nc, index, n, scale_exp, codes.data_ptr(),

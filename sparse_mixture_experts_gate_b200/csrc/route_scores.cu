@@ -30,9 +30,9 @@
 // keys, and 2^-23 of the keys for adding the biases; a group's score has two of them.
 // Logits themselves as keys are exact.
 //
-// What bounds it: the instructions, about 800 a token for 256 experts in 8 groups,
-// 8 selected, sigmoids and a bias (32768 tokens: 41 us, the issue slots 67% taken and the
-// ALU 60%, where reading the logits takes 7; 17 us for one expert of 256 by its logit).
+// What bounds it: the instructions, about 810 a token for 256 experts in 8 groups,
+// 8 selected, sigmoids and a bias (32768 tokens: 41 us, the issue slots 66% taken and the
+// ALU 58%, where reading the logits takes 7; 17 us for one expert of 256 by its logit).
 #include <algorithm>
 #include <type_traits>
 

@@ -35,9 +35,13 @@ class RouteConfig:
         if score not in B.MOE_SCORE:
             raise ValueError(f"unknown score {score!r}")
         self.num_experts, self.num_active = num_experts, num_active
+        self._args = (num_experts, num_active, score, num_groups, top_groups, group_top, renormalize, scale)
         self.struct = B.MoeRouteConfig(num_experts, num_active, B.MOE_SCORE[score], num_groups, top_groups, group_top,
                                        int(renormalize), scale, B.MOE_DTYPE["fp32"])
         self._at = ctypes.addressof(self.struct)
+
+    def __reduce__(self):  # a copy has a struct, and so an address, of its own
+        return RouteConfig, self._args
 
 
 def route(logits: torch.Tensor, cfg: RouteConfig, bias: Optional[torch.Tensor] = None, counts: bool = True,

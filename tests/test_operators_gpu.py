@@ -215,6 +215,10 @@ ROUTES = [
     (40, 512, 32, "softmax", 32, 9, 2, True, 1.0, False),
     (31, 100, 10, "sigmoid", 20, 10, 2, False, 1.0, True),
     (17, 16, 16, "sigmoid", 16, 16, 2, True, 1.0, False),
+    (50, 128, 8, "sigmoid", 4, 2, 2, True, 1.0, True),
+    (50, 64, 4, "softmax", 2, 1, 1, False, 1.0, False),
+    (45, 512, 8, "sigmoid", 16, 4, 2, True, 2.5, True),
+    (45, 32, 5, "sigmoid", 32, 7, 2, True, 1.0, True),
 ]
 
 
@@ -426,7 +430,7 @@ def _check_product(got, want, mass, K, act, bf16):
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
-@pytest.mark.parametrize("R,N,K", [(1, 128, 256), (8, 128, 64), (16, 256, 128), (128, 128, 256), (3, 5, 32), (130, 77, 96),
+@pytest.mark.parametrize("R,N,K", [(1, 128, 256), (8, 128, 64), (16, 256, 128), (128, 128, 256), (3, 5, 32), (1, 1, 32), (130, 1, 96), (130, 77, 96),
                                    (65, 129, 320), (191, 64, 1056), (192, 384, 512), (193, 130, 2048), (500, 257, 416),
                                    (1000, 640, 7168)])
 def test_product_of_one_group(fmt, R, N, K):

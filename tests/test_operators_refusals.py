@@ -1,5 +1,7 @@
 """Argument checks of the layer-free operators, on the host, before anything is enqueued (no GPU)."""
+import copy
 import ctypes
+import pickle
 import math
 
 import pytest
@@ -171,6 +173,12 @@ def test_python_refusals():
     a, w = ops.MxTensor("mxfp4", codes, scales, 2, 64), ops.MxTensor("nvfp4", codes, scales, 2, 64)
     with pytest.raises(ValueError, match="differ"):
         ops.mx_gemm(a, w)
+
+
+def test_copies_of_a_routing_are_whole():
+    cfg = ops.RouteConfig(60, 6, "sigmoid", 4, 2, 1, False, 2.5)
+    for c in (copy.copy(cfg), copy.deepcopy(cfg), pickle.loads(pickle.dumps(cfg))):
+        assert c._at == ctypes.addressof(c.struct) != cfg._at and bytes(c.struct) == bytes(cfg.struct)
 
 
 def test_reference_rounds_as_the_formats_say():

@@ -27,7 +27,8 @@
 // division) and, but for the sum, which all keys share, by 2^-20 down to e^-16 of the
 // largest. So keys without a bias are in order if 2^-18 of themselves apart; with one
 // the error counts absolutely, twice 2^-22 or 2^-19 of the largest score for two
-// keys, and 2^-23 of the keys for adding the biases; a group's score has two of them.
+// keys, and 2^-24 of each key for adding the biases; a group's score has the errors of
+// the two keys that it is the sum of, each at its key's size.
 // Logits themselves as keys are exact.
 //
 // What bounds it: the instructions, about 810 a token for 256 experts in 8 groups,
@@ -336,7 +337,7 @@ __device__ __forceinline__ bool route_fast(float (&h)[RE], const float *bias, co
         __syncwarp();
         for (int off = 1; off < gr.width; off <<= 1)
             merge_top2(t1, t2, __shfl_xor_sync(0xffffffffu, t1, off), __shfl_xor_sync(0xffffffffu, t2, off));
-        const float mine = a.group_top == 2 && t2 != -INFINITY ? t1 + t2 : t1;
+        const float u2 = a.group_top == 2 && t2 != -INFINITY ? t2 : 0.f, mine = t1 + u2;
         // Scores with the group's index in the lowest bits: the check below sees to those that this puts out
         // of order.
         const uint32_t rank = (key_code(mine) & ~31u) | (31u - gr.g);
@@ -349,9 +350,12 @@ __device__ __forceinline__ bool route_fast(float (&h)[RE], const float *bias, co
         const bool there = gr.g < a.groups, chosen = there && before < a.top_groups;
         const uint32_t lanes = __ballot_sync(0xffffffffu, chosen);
         if (a.top_groups < a.groups) {
-            // The lowest group inside against the highest one outside.
-            const float in = -warp_max(chosen ? -mine : -INFINITY), out = warp_max(there && !chosen ? mine : -INFINITY);
-            if (out != -INFINITY && !(in - out > 2.f * apart + 0x1p-22f * (fabsf(in) + fabsf(out)))) sure = false;
+            // The lowest group inside against the highest one outside, each as far off as it can be: its keys
+            // were rounded at their own size, of which their sum says nothing where they have opposite signs. That
+            // and the sum's rounding come to 2^-23 (|t1| + |u2|); 2^-22 holds the rounding of the bounds too.
+            const float off = fabsf(mine) == INFINITY ? 0.f : 0x1p-22f * (fabsf(t1) + fabsf(u2));
+            const float in = -warp_max(chosen ? off - mine : -INFINITY), out = warp_max(there && !chosen ? mine + off : -INFINITY);
+            if (out != -INFINITY && !(in - out > 2.f * apart)) sure = false;
         }
 #pragma unroll
         for (int q = 0; q < RE; ++q)

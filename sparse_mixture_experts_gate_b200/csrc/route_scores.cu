@@ -337,7 +337,8 @@ __device__ __forceinline__ bool route_fast(float (&h)[RE], const float *bias, co
         __syncwarp();
         for (int off = 1; off < gr.width; off <<= 1)
             merge_top2(t1, t2, __shfl_xor_sync(0xffffffffu, t1, off), __shfl_xor_sync(0xffffffffu, t2, off));
-        const float u2 = a.group_top == 2 && t2 != -INFINITY ? t2 : 0.f, mine = t1 + u2;
+        // Half a group's score, which does not leave the range where the lowest finite numbers are added up.
+        const float h1 = 0.5f * t1, h2 = a.group_top == 2 && t2 != -INFINITY ? 0.5f * t2 : 0.f, mine = h1 + h2;
         // Scores with the group's index in the lowest bits: the check below sees to those that this puts out
         // of order.
         const uint32_t rank = (key_code(mine) & ~31u) | (31u - gr.g);
@@ -352,10 +353,10 @@ __device__ __forceinline__ bool route_fast(float (&h)[RE], const float *bias, co
         if (a.top_groups < a.groups) {
             // The lowest group inside against the highest one outside, each as far off as it can be: its keys
             // were rounded at their own size, of which their sum says nothing where they have opposite signs. That
-            // and the sum's rounding come to 2^-23 (|t1| + |u2|); 2^-22 holds the rounding of the bounds too.
-            const float off = fabsf(mine) == INFINITY ? 0.f : 0x1p-22f * (fabsf(t1) + fabsf(u2));
+            // and the sum's rounding come to 2^-23 (|h1| + |h2|); 2^-22 holds the rounding of the bounds too.
+            const float off = fabsf(mine) == INFINITY ? 0.f : 0x1p-22f * (fabsf(h1) + fabsf(h2));
             const float in = -warp_max(chosen ? off - mine : -INFINITY), out = warp_max(there && !chosen ? mine + off : -INFINITY);
-            if (out != -INFINITY && !(in - out > 2.f * apart)) sure = false;
+            if (out != -INFINITY && !(in - out > apart)) sure = false;
         }
 #pragma unroll
         for (int q = 0; q < RE; ++q)

@@ -74,3 +74,17 @@ def test_groups_forced_in_and_out(group_top):
     bias[:8], bias[8:16], bias[16:24] = 1e4, -1e4, 3e6
     bias[60] = math.inf
     check(logits, 8, "sigmoid", 8, 4, group_top, bias)
+
+
+@pytest.mark.parametrize("group_top", [1, 2])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_groups_of_the_lowest_numbers(score, group_top):
+    """Experts that the lowest finite number takes out come before those that are not there, also as groups."""
+    g = gen(8)
+    logits = torch.randn(400, 64, generator=g, device="cuda")
+    logits[:, :16] = -math.inf
+    logits[200:, 16:24] = -math.inf
+    bias = torch.zeros(64, device="cuda")
+    bias[16:56] = torch.finfo(torch.float32).min
+    for top in (1, 2, 3, 5):
+        check(logits, min(12, 8 * top), score, 8, top, group_top, bias)

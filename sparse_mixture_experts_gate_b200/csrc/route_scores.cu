@@ -409,8 +409,10 @@ __device__ __forceinline__ bool route_fast(float (&h)[RE], const float *bias, co
         bool fine = lane >= a.k || next == -INFINITY || v - next > error;
         if (!__all_sync(0xffffffffu, fine || lane != a.k - 1)) {
             // The first one left out may be as high as the lowest choice by its code: its whole key counts, if
-            // no other one has the same code.
-            const uint32_t rest = __reduce_max_sync(0xffffffffu, code[0] == left ? (RE > 1 ? code[1] : 0u) : code[0]);
+            // no other one has the same code. Behind the codes that the rounds moved up, a lane has those that they
+            // did not reach (code[kDepth], up to 8 choices).
+            const uint32_t behind = max(RE > 1 ? code[1] : 0u, RE > kDepth ? code[RE > kDepth ? kDepth : 0] : 0u);
+            const uint32_t rest = __reduce_max_sync(0xffffffffu, code[0] == left ? behind : code[0]);
             if (lane == a.k - 1)
                 fine = (rest & ~kLow) < (left & ~kLow) && v - keys[padded(static_cast<int>(kLow - (left & kLow)))] > error;
         }

@@ -88,3 +88,35 @@ def test_groups_of_the_lowest_numbers(score, group_top):
     bias[16:56] = torch.finfo(torch.float32).min
     for top in (1, 2, 3, 5):
         check(logits, min(12, 8 * top), score, 8, top, group_top, bias)
+
+
+def test_border_hidden_behind_a_lanes_other_choices():
+    """Experts 0, 32 and 64 lead; the fourth choice is one of 1, 96 and 128, whose fp32 keys share the bits that
+    are sorted. 96 and 128 are the fourth and fifth of one lane's experts."""
+    key = torch.full((256,), 0.5, dtype=torch.float64)
+    for e, v in ((0, 0.92), (32, 0.91), (64, 0.90), (1, 0.750003), (96, 0.750001), (128, 0.750008)):
+        key[e] = v
+    logits = torch.zeros(3, 256, device="cuda")
+    bias = (key - 0.5).float().cuda()
+    check(logits, 4, "sigmoid", bias=bias)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("groups", [1, 2])
+@pytest.mark.parametrize("E", [200, 256, 384, 512])
+@pytest.mark.parametrize("k", [4, 6, 8, 12])
+def test_near_ties_of_experts_32_apart(k, E, groups, score):
+    """The highest keys of a token belong to experts that are congruent modulo 32, all but the first three
+    within the bits that fp32 keys are sorted without."""
+    g = gen(E + k)
+    T = 4096
+    first = torch.randint(0, 32, (T, 1), generator=g, device="cuda")
+    lanes = torch.arange(E, device="cuda") % 32 == first
+    close = lanes | (torch.rand(T, E, generator=g, device="cuda") < 4.0 / E)
+    u = torch.rand(T, E, generator=g, device="cuda", dtype=torch.float64)
+    key = torch.where(close, 0.75 + 2.0 ** -15 * u, 0.1 + 0.4 * u)
+    # Three of the lane's experts stand clear of the others.
+    high = torch.where(lanes, u, -1.0).topk(3, dim=1).indices
+    key.scatter_(1, high, 0.8 + 0.1 * torch.rand(T, 3, generator=g, device="cuda", dtype=torch.float64))
+    logits = (torch.log(key / (1 - key)) if score == "sigmoid" else torch.log(key)).float()
+    check(logits, k, score, groups, groups, 2, torch.zeros(E, device="cuda"))

@@ -21,13 +21,16 @@
 //                of these (or two groups at the border of the selection) are closer
 //                together than their error: 0.1% to 0.5% of the tokens for normal
 //                logits and 256 experts.
-// Bounds that route_fast relies on: a sigmoid is off by 2^-22 (__expf's 2 + 1.2 |l|
-// ulp times s (1 - s), and the reciprocal), and above e^-16 by 2^-19 of itself; a
-// softmax by 2^-19 of itself (the sum of at most 512 terms in 16 + 5 steps, expf, the
-// division) and, but for the sum, which all keys share, by 2^-20 down to e^-16 of the
-// largest. So keys without a bias are in order if 2^-18 of themselves apart; with one
-// the error counts absolutely, twice 2^-22 or 2^-19 of the largest score for two
-// keys, and 2^-24 of each key for adding the biases; a group's score has the errors of
+// Bounds that route_fast relies on, from CUDA's error bounds of the functions:
+//   a sigmoid 1 / (1 + x): x = __expf(-l) is off by 2 + 1.173 |l| ulp, the sum by half an
+//     ulp, __fdividef by 2. Of itself s is off by (1 - s)(2 + 1.173 |l|) 2^-23 + 2.5 x 2^-23,
+//     above e^-16 22.5 x 2^-23 < 2^-18; in all by 1.91 x 2^-23 < 2^-22 (the most, near l = 1);
+//   a softmax, 2^-19 of itself (the sum of at most 512 terms in 16 + 5 steps, expf, the
+//     division) and, but for the sum, which all keys share, 1.4 x 2^-20 down to e^-16 of the
+//     largest (rounding l - m 2^-20, expf 2^-22, the product 2^-24).
+// So keys without a bias are in order if 2^-17 (sigmoid) or 2^-18 (softmax) of themselves
+// apart; with one the error counts absolutely, twice 2^-22 or 2^-19 of the largest score for
+// two keys, and 2^-24 of each key for adding the biases; a group's score has the errors of
 // the two keys that it is the sum of, each at its key's size.
 // Logits themselves as keys are exact.
 //
@@ -405,7 +408,7 @@ __device__ __forceinline__ bool route_fast(float (&h)[RE], const float *bias, co
         v = choice >= 0 ? v : -INFINITY;
         float next = __shfl_down_sync(0xffffffffu, v, 1);
         if (lane == a.k - 1) next = left >= kNone ? code_key(left | kLow) : -INFINITY;
-        const float error = a.bias ? apart + 0x1p-23f * fabsf(v) : 0x1p-18f * v;
+        const float error = a.bias ? apart + 0x1p-23f * fabsf(v) : (SIGMOID ? 0x1p-17f : 0x1p-18f) * v;
         bool fine = lane >= a.k || next == -INFINITY || v - next > error;
         if (!__all_sync(0xffffffffu, fine || lane != a.k - 1)) {
             // The first one left out may be as high as the lowest choice by its code: its whole key counts, if

@@ -120,3 +120,15 @@ def test_near_ties_of_experts_32_apart(k, E, groups, score):
     key.scatter_(1, high, 0.8 + 0.1 * torch.rand(T, 3, generator=g, device="cuda", dtype=torch.float64))
     logits = (torch.log(key / (1 - key)) if score == "sigmoid" else torch.log(key)).float()
     check(logits, k, score, groups, groups, 2, torch.zeros(E, device="cuda"))
+
+
+@pytest.mark.parametrize("groups,top", [(2, 2), (8, 4), (16, 16)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_small_sigmoid_scores_close_together(dtype, groups, top):
+    """Scores without a bias between e^-16 and e^-12, apart by about the error that fp32 has there."""
+    g = gen(groups)
+    T, E = 20000, 128
+    base = -16 + 4 * torch.rand(T, 1, generator=g, device="cuda")
+    step = torch.randint(-40, 41, (T, E), generator=g, device="cuda") * 2.0 ** -20
+    logits = torch.where(torch.rand(T, E, generator=g, device="cuda") < 0.3, base * (1 + step / 16), base - 3)
+    check(logits.to(dtype), 8, "sigmoid", groups, top)

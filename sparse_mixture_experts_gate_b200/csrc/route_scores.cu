@@ -218,10 +218,15 @@ __device__ __forceinline__ int2 route_exact(const XT *src, double *row, const Ro
         return make_int2(choice, __float_as_int(sf * a.scale));
     }
     double s = 0.0;
-    if (choice >= 0) s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)m) / z;
     if (a.renormalize) {
+        // Over e^top, the largest of the selection's e^l (softmax) or e^min(l, 0) (sigmoid, which is that over
+        // 1 + e^-|l|): scores that are nothing in 64 bits still have their shares.
+        const float x = a.sigmoid ? fminf(l, 0.f) : l, top = warp_max(x);  // l: -inf without a choice
+        if (choice >= 0) s = exp((double)x - (double)top) / (a.sigmoid ? 1.0 + exp(-fabs((double)l)) : 1.0);
         const double sum = warp_sum(s);
         s = sum > 0.0 ? s / sum : 0.0;
+    } else if (choice >= 0) {
+        s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)m) / z;
     }
     return make_int2(choice, __float_as_int(static_cast<float>(s * (double)a.scale)));
 }

@@ -604,7 +604,14 @@ __global__ void __launch_bounds__(kBackThreads) route_backward_kernel(const __gr
             const float s = live ? (l >= 0.f ? r : en * r) : 0.f, ds = live ? (l >= 0.f ? en * r : r) : 0.f;  // s, 1 - s
             d = g * s * ds;
             if (a.renormalize) {
-                const float total = sum(s), w = total > 0.f ? s / total : 0.f;
+                float x = s, total = sum(s);
+                if (!(total > 0x1p-80f)) {
+                    // Scores so small that fp32 loses them: s is e^min(l, 0) r, here over the largest e^min(l, 0).
+                    const float low = fminf(l, 0.f), top = warp_max(low);
+                    x = live ? expf(low - top) * r : 0.f;
+                    total = sum(x);
+                }
+                const float w = total > 0.f ? x / total : 0.f;
                 d = w * (g - sum(g * w)) * ds;
             }
         } else {  // the softmax over the selection alone

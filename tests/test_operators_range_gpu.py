@@ -28,6 +28,34 @@ def small_weights(logits, idx):
     return torch.softmax(torch.nn.functional.logsigmoid(logits.double()).gather(1, idx.long()), 1)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("at", [-60.0, -87.5, -95.0, -104.0, -300.0, -1e4])
+def test_gradient_of_small_sigmoid_scores(at, dtype):
+    """Renormalised weights have a gradient of ordinary size however small their scores are."""
+    g = gen(1)
+    logits = (at + torch.randn(40, 16, generator=g, device="cuda")).to(dtype)
+    cfg = ops.RouteConfig(16, 4, "sigmoid", scale=2.5)
+    idx = logits.float().topk(4, dim=1).indices.to(torch.int32)
+    gw = torch.randn(40, 4, generator=g, device="cuda")
+    d = ops.route_backward(gw, logits, idx, cfg)
+    l = logits.double().requires_grad_()
+    (2.5 * small_weights(l, idx) * gw).sum().backward()
+    tol = G_TOL * 2.5 * gw.abs().max() + (2.0 ** -8 * l.grad.abs() if dtype == torch.bfloat16 else 0)
+    assert ((d.double() - l.grad).abs() <= tol).all()
+
+
+def test_gradient_of_sigmoid_scores_of_every_size():
+    """Scores next to 0 and next to 1 in one selection, and selections of masked logits only."""
+    logits = torch.tensor([[-120.0, -118.5, -3.0, 2.0], [50.0, 90.0, 130.0, 88.0], [-89.0, -90.0, -91.0, 0.0],
+                           [-math.inf, -100.0, -101.0, -math.inf], [-math.inf] * 4], device="cuda")
+    idx = torch.tensor([[0, 1], [0, 2], [0, 1], [1, 2], [0, 3]], dtype=torch.int32, device="cuda")
+    gw = torch.tensor([[1.0, -2.0]], device="cuda").expand(5, 2).contiguous()
+    d = ops.route_backward(gw, logits, idx, ops.RouteConfig(4, 2, "sigmoid"))
+    l = logits[:4].double().requires_grad_()
+    (small_weights(l, idx[:4]) * gw[:4]).sum().backward()
+    assert ((d[:4].double() - l.grad).abs() <= G_TOL * 2).all() and (d[4] == 0).all()
+
+
 @pytest.mark.parametrize("at", [-60.0, -95.0, -700.0, -745.0, -800.0, -1e4, LOWEST])
 def test_renormalised_weights_of_small_sigmoid_scores(at):
     """They sum to the scale, even where every score is 0 in 64 bits."""

@@ -7,7 +7,8 @@
 // A block with an infinity or a NaN gets the NaN scale and zero codes. Where
 // an NVFP4 scale rounds to 0 the codes are 0.
 //
-// Every rounding is the one of the exact quotient. MXFP4 quotients are exact.
+// Every rounding is the one of the exact quotient. MXFP4 quotients are exact: x / scale 2^-e, in this
+// order, as u itself may be below fp32's normal numbers.
 // NVFP4 divides fp32 elements (correctly rounded: a quotient that is not one of
 // the rounding borders cannot round onto one, as border times scale has at most
 // 7 significant bits). For bf16 elements the quotient times 1 / scale is off by
@@ -195,8 +196,9 @@ __device__ __forceinline__ uint2 quantize16(const Raw<XT> &v, float pre, uint32_
         byte = finite ? static_cast<uint32_t>(e > 0 ? e : 0) : 255u;
         scale = e8m0_value(byte);
         const float inv = __uint_as_float((254u - min(byte, 253u)) << 23);
+        // The scale first: what 2^-e alone would make too small for fp32's normal numbers keeps its digits.
 #pragma unroll
-        for (int i = 0; i < kLaneElems; ++i) u[i] = PRE ? element<XT>(v, i) * pre * inv : element<XT>(v, i) * inv;
+        for (int i = 0; i < kLaneElems; ++i) u[i] = PRE ? element<XT>(v, i) * inv * pre : element<XT>(v, i) * inv;
     } else {
         byte = finite ? e4m3_of(__fdiv_rn(__uint_as_float(top), 6.f)) : 0u;
         scale = e4m3_finite(byte);

@@ -9,6 +9,7 @@ import math
 import pytest
 import torch
 
+import operators_ref as ref
 from sparse_mixture_experts_gate_b200 import operators as ops
 
 pytestmark = pytest.mark.gpu
@@ -79,3 +80,22 @@ def test_renormalised_weights_far_below_the_largest_score(gap):
     assert (idx == torch.tensor([28, 29, 30], dtype=torch.int32, device="cuda")).all()
     want = torch.softmax(logits.double()[:, 28:31], 1)
     assert ((w.double() - want).abs() <= W_TOL * want).all()
+
+
+def test_mxfp4_borders_below_the_normal_numbers():
+    """x 2^-60 lies among fp32's subnormals: the code is still that of the exact quotient."""
+    unit = 2.0 ** -67  # a scale of 2^-127 times 2^60
+    row = []
+    for border in (0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0):
+        bits = torch.tensor([border * unit]).view(torch.int32)
+        row += [(bits + s).view(torch.float32).item() for s in (-1, 0, 1)]
+    x = torch.zeros(2, 32)
+    x[0, :21], x[0, 31] = torch.tensor(row), 6 * unit
+    x[1] = -x[0]
+    x = x.cuda()
+    v = torch.empty_like(x)
+    q = ops.mx_quantize(x, "mxfp4", scale_exp=60, values=v)
+    codes, byte, want = ref.quantize(x, "mxfp4", 60)
+    assert torch.equal(ref.scale_bytes(q.scales, 2, 32, "mxfp4"), byte)
+    assert torch.equal(ref.unpack(q.codes), codes)
+    assert torch.equal(v.double(), want) and torch.equal(ops.mx_dequantize(q).double(), want)

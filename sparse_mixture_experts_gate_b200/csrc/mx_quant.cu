@@ -273,12 +273,11 @@ __global__ void __launch_bounds__(kThreads) mx_quantize_kernel(const MxQuantArgs
                 *reinterpret_cast<uint2 *>(codes + kStep / 2 * s) = code;
                 if (a.values) {
                     float o[kLaneElems];
-                    const float m = scale * a.post;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float2 q = e2m1x2_values((i < 4 ? code.x : code.y) >> (8 * (i % 4)) & 0xffu);
-                        o[2 * i] = q.x * m;
-                        o[2 * i + 1] = q.y * m;
+                        o[2 * i] = PRE ? q.x * a.post * scale : q.x * scale;  // in this order: as mx_dequantize_kernel
+                        o[2 * i + 1] = PRE ? q.y * a.post * scale : q.y * scale;
                     }
                     store16<XT>(static_cast<XT *>(a.values) + (int64_t)r * a.values_ld + c, vec_values, o);
                 }
@@ -287,6 +286,8 @@ __global__ void __launch_bounds__(kThreads) mx_quantize_kernel(const MxQuantArgs
     }
 }
 
+// A value is code 2^e scale, in this order: 2^e times the scale alone may leave fp32's range although the value
+// does not, or is 0.
 template <int FMT, typename OT>
 __global__ void __launch_bounds__(kThreads) mx_dequantize_kernel(const MxDequantArgs a, bool vec) {
     const int per_row = a.cols / 8;
@@ -296,14 +297,14 @@ __global__ void __launch_bounds__(kThreads) mx_dequantize_kernel(const MxDequant
     const int c = static_cast<int>(i - r * per_row) * 8, j = c / MxFormat<FMT>::kBlock;
     const int SB = mx_scale_tiles(a.cols, MxFormat<FMT>::kBlock);
     const uint32_t byte = a.scales[(r / 128 * SB + j / 4) * 512 + (r % 32) * 16 + (r % 128 / 32) * 4 + j % 4];
-    const float m = (FMT == kMxFp4 ? e8m0_value(byte) : e4m3_value(byte)) * a.post;
+    const float scale = FMT == kMxFp4 ? e8m0_value(byte) : e4m3_value(byte);
     const uint32_t code = *reinterpret_cast<const uint32_t *>(a.codes + r * (a.cols / 2) + c / 2);
     float o[8];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const float2 q = e2m1x2_values(code >> (8 * k) & 0xffu);
-        o[2 * k] = q.x * m;
-        o[2 * k + 1] = q.y * m;
+        o[2 * k] = q.x * a.post * scale;
+        o[2 * k + 1] = q.y * a.post * scale;
     }
     store8<OT>(static_cast<OT *>(a.out) + r * a.ld + c, vec, o);
 }

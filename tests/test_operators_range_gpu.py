@@ -99,3 +99,28 @@ def test_mxfp4_borders_below_the_normal_numbers():
     assert torch.equal(ref.scale_bytes(q.scales, 2, 32, "mxfp4"), byte)
     assert torch.equal(ref.unpack(q.codes), codes)
     assert torch.equal(v.double(), want) and torch.equal(ops.mx_dequantize(q).double(), want)
+
+
+@pytest.mark.parametrize("exp", [-60, -1, 0, 60])
+def test_values_of_the_smallest_numbers(exp):
+    """Multiples of fp32's smallest number: their scales times 2^exp may be smaller than it, their values are not."""
+    x = torch.arange(1, 65, dtype=torch.float32).view(2, 32).repeat(3, 1)
+    x[2:4] = x[2:4].remainder(3)
+    x[4:6] = 1.0
+    x = (x.double() * 2.0 ** -149).float().cuda()
+    v = torch.empty_like(x)
+    q = ops.mx_quantize(x, "mxfp4", scale_exp=exp, values=v)
+    codes, byte, want = ref.quantize(x, "mxfp4", exp)
+    assert torch.equal(ref.unpack(q.codes), codes) and torch.equal(ref.scale_bytes(q.scales, 6, 32, "mxfp4"), byte)
+    assert torch.equal(v.double(), want.float().double()) and torch.equal(ops.mx_dequantize(q), v)
+
+
+def test_values_of_the_largest_scales():
+    """2^127 times 2^60 is out of range: zero codes are still zeros, and small exponents bring the others back."""
+    codes = torch.arange(16, dtype=torch.uint8).repeat(4)
+    packed = (codes[0::2] | codes[1::2] << 4).view(1, 32).cuda()
+    byte = torch.full((1, 1, 2), 254, dtype=torch.uint8, device="cuda")
+    for exp in (-60, 0, 60):
+        q = ops.MxTensor("mxfp4", packed, ops.mx_tile_scales(byte), 1, 64, scale_exp=exp)
+        want = ref.values(codes[None].cuda(), byte[0], "mxfp4", exp).float()
+        assert torch.equal(ops.mx_dequantize(q), want)

@@ -432,6 +432,9 @@ class MoELayer:
         self.handle = moe_layer_create(cfg, self._cw)
         self._ws = None
         self._ws_T = -1
+        self._mx = self._mx_stream = None  # the 4-bit weights' buffer, the stream that wrote it,
+        self._mx_kept = []                 # buffers that a capture replaced,
+        self._streams = set()              # and the streams of the forwards since
         self._dt = torch.bfloat16 if w.dtype == "bf16" else torch.float32
 
     def close(self):
@@ -468,22 +471,40 @@ class MoELayer:
         """Run the experts in 4 bits (moe_prepare_experts_mx): w1 and w2 are quantised
         into a buffer this object keeps. The exponents of "nvfp4" weights are those of
         weights of variance 1 / fan-in unless given. fmt None returns to bf16. Call it
-        between forwards, and again after changing the weights; StepGraphs and
-        HostPipelines made before it keep what they were captured with, and must not
-        be used any more."""
+        between forwards, and again after changing the weights. It is enqueued on `stream`:
+        forwards on other streams have to be ordered after it there. Where there are 4-bit
+        weights that forwards on other streams may still read, it waits for the device.
+        StepGraphs and HostPipelines made before it keep what they were captured with, and
+        must not be used any more."""
         import math
         import torch
         s = stream if stream is not None else torch.cuda.current_stream(self.device).cuda_stream
         if fmt is None:
             moe_prepare_experts_mx(self.handle, 0, 0, 0, None, 0, s)
-            self._mx = None
+            self._replace_mx(None, None)
             return
         exps = [e if e is not None else (round(-0.5 * math.log2(n)) if fmt == "nvfp4" else 0)
                 for e, n in ((w1_exp, self.w.d), (w2_exp, self.w.F))]
         n = moe_experts_mx_bytes(self.handle, MOE_MX[fmt])
-        buf = torch.empty(max(n, 256), dtype=torch.uint8, device=self.device)
+        # The buffer is the writing stream's: memory of another one might still be in use there.
+        with torch.cuda.stream(torch.cuda.ExternalStream(s, self.device)):
+            buf = torch.empty(max(n, 256), dtype=torch.uint8, device=self.device)
         moe_prepare_experts_mx(self.handle, MOE_MX[fmt], exps[0], exps[1], buf.data_ptr(), buf.numel(), s)
-        self._mx = buf
+        self._replace_mx(buf, s)
+
+    def _replace_mx(self, buf, stream):
+        """Lets go of the previous 4-bit weights. Their memory goes back to the stream that wrote them, so
+        forwards on others have to have read them before: the host waits for the device, or, while a graph is
+        captured and nothing may wait, keeps them."""
+        import torch
+        if self._mx is not None and self._streams - {self._mx_stream}:
+            if torch.cuda.is_current_stream_capturing():
+                self._mx_kept.append(self._mx)
+            else:
+                torch.cuda.synchronize(self.device)
+                self._mx_kept.clear()
+        self._mx, self._mx_stream = buf, stream
+        self._streams.clear()
 
     def workspace(self, T: int):
         import torch
@@ -529,6 +550,8 @@ class MoELayer:
             routing = MoeRouting(_ptr(out["logits"]), _ptr(out["gates"]), _ptr(out["topk_idx"]), _ptr(out["slot"]),
                                  _ptr(out["count_pre"]), _ptr(out["count_kept"]))
         moe_forward(self.handle, _ptr(x), T, _ptr(noise), ws.data_ptr(), ws.numel(), _ptr(out["y"]), routing, s)
+        if self._mx is not None:
+            self._streams.add(s)
         return out
 
     def aux_stats(self, out, token_loss=None, stream=None):

@@ -514,8 +514,8 @@ MOE_API int moe_mx_dequantize(int32_t format, const void *codes, const void *sca
  *   scale_exp          -120..120, the sum of both operands' exponents
  *   activation         MOE_ACT_*, MOE_ACT_NONE = none
  *   out                rows of n, out_ld apart, out_dtype MOE_DTYPE_*
- *   status             device word or NULL: bits are or-ed in (bit 0: a bounded
- *                      wait gave up, out is incomplete; bit 1 as above)
+ *   status             device word: bits are or-ed in (bit 0: a bounded wait gave up,
+ *                      out is incomplete; bit 1 as above). NULL: moe_mx_status tells
  * groups <= 1024, groups x n < 2^31 - 1024, and groups (rows / 192 + 1) n / 256 (short
  * segments, rows < 192 groups: / 64 and / 128) below about 2^31. rows = 0 enqueues nothing. Needs no
  * workspace; calls on any streams may overlap. Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
@@ -530,6 +530,12 @@ typedef struct {
     uint32_t *status;
 } moe_mx_gemm_t;
 MOE_API int moe_mx_gemm(const moe_mx_gemm_t *args, void *stream);
+
+/* Whether the products without a status word that have ended on the current device did
+ * all of their work: synchronises `stream` (which may not be captured), then returns MOE_OK,
+ * MOE_ERR_TIMEOUT if a bounded device-side wait gave up, or MOE_ERR_INVALID_ARG if a segment
+ * broke its bounds, in any of them since the last call that said so; or MOE_ERR_CUDA. */
+MOE_API int moe_mx_status(void *stream);
 
 /* 4-bit experts of a bf16 layer with ep_size 1 (shared experts included): quantises
  * w1 and w2 once, enqueued on `stream`, into `buffer` (device, caller-owned, >=

@@ -31,7 +31,7 @@ EXPORTS = ("moe_config_default", "moe_layer_create", "moe_workspace_bytes", "moe
            "moe_selftest_router_timeout", "moe_router_planes_bytes", "moe_prepare_router",
            "moe_ep_dispatch", "moe_ep_layout", "moe_ep_experts_workspace_bytes", "moe_ep_experts", "moe_ep_combine", "moe_device_status", "moe_set_timing_events", "moe_launch_count", "moe_destroy", "moe_status_string",
            "moe_last_error", "moe_route_config_default", "moe_route", "moe_route_backward", "moe_mx_codes_bytes",
-           "moe_mx_scales_bytes", "moe_mx_quantize", "moe_mx_once_bytes", "moe_mx_quantize_once", "moe_mx_gather", "moe_mx_dequantize", "moe_mx_gemm", "moe_set_routing",
+           "moe_mx_scales_bytes", "moe_mx_quantize", "moe_mx_once_bytes", "moe_mx_quantize_once", "moe_mx_gather", "moe_mx_dequantize", "moe_mx_gemm", "moe_mx_status", "moe_set_routing",
            "moe_experts_mx_bytes", "moe_prepare_experts_mx")
 
 
@@ -172,6 +172,8 @@ def lib() -> ctypes.CDLL:
         L.moe_mx_dequantize.argtypes = [i32, vp, vp, i32, i32, i32, vp, i32, i64, vp]
         L.moe_mx_gemm.restype = ctypes.c_int
         L.moe_mx_gemm.argtypes = [ctypes.POINTER(MoeMxGemm), vp]
+        L.moe_mx_status.restype = ctypes.c_int
+        L.moe_mx_status.argtypes = [vp]
         L.moe_set_routing.restype = ctypes.c_int
         L.moe_set_routing.argtypes = [vp, ctypes.POINTER(MoeRouteConfig)]
         L.moe_experts_mx_bytes.restype = sz
@@ -352,6 +354,10 @@ def moe_mx_dequantize(fmt: int, codes: Optional[int], scales: Optional[int], row
 
 def moe_mx_gemm(args: MoeMxGemm, stream: int) -> int:
     return _check(lib().moe_mx_gemm(ctypes.byref(args), stream), "moe_mx_gemm")
+
+
+def moe_mx_status(stream: int) -> int:
+    return _check(lib().moe_mx_status(stream), "moe_mx_status")
 
 
 def moe_set_routing(layer: int, cfg: Optional[MoeRouteConfig]) -> int:

@@ -87,7 +87,7 @@ struct MxGemmArgs {
     int out_f32;
     int64_t out_ld;
     int vec_ok;          // bf16 outputs: out and out_ld allow 16-byte stores
-    uint32_t *status;    // or null
+    uint32_t *status;    // or null: the device's word for all such products
 };
 // Tensor maps of the codes (boxes of 128 bytes x 128 weight rows, 16 or 96 token
 // rows) and of the scale tiles (boxes of one stage's tiles of one row block).
@@ -99,6 +99,9 @@ bool mx_gemm_narrow(const MxGemmArgs &a);
 bool encode_mx_maps(MxMaps *m, bool narrow, int format, const void *a_codes, const void *a_scales, uint64_t rows, const void *w_codes,
                     const void *w_scales, uint64_t groups, int n, int k);
 cudaError_t launch_mx_gemm(const MxMaps &m, const MxGemmArgs &a, int format, int num_sms, cudaStream_t s);
+
+// Waits for the stream, reads the current device's word and clears the bits that were set.
+cudaError_t mx_take_status(uint32_t *bits, cudaStream_t s);
 
 // Device status bits the product adds to kDevTimeout.
 enum : uint32_t { kDevBadGroup = 2u };

@@ -90,6 +90,9 @@ struct Cfg {
     static_assert(kSub % 1024 == 0, "operand tiles keep the 1024-byte swizzle alignment");
 };
 
+// Status bits of the products that were given no word of their own, until mx_take_status reads them.
+__device__ uint32_t g_unclaimed_status;
+
 struct Unit {
     int g, row0, ntok, feat0;
 };
@@ -523,11 +526,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (CG == 2) tmem_dealloc_pair(tmem_base, kTmemCols);
         else tmem_dealloc(tmem_base, kTmemCols);
     }
-    if (threadIdx.x == 0 && a.status) {
+    if (threadIdx.x == 0) {
         const uint32_t v = *status | bad;
-        if (v) atomicOr(a.status, v);
+        if (v) atomicOr(a.status ? a.status : &g_unclaimed_status, v);
     }
 }
+
+__global__ void clear_status_kernel(uint32_t bits) { atomicAnd(&g_unclaimed_status, ~bits); }
 
 template <int FMT, int TILE, int SUB, int CG, int ACT>
 cudaError_t launch(const MxMaps &m, const MxGemmArgs &a, int num_sms, cudaStream_t s) {
@@ -568,6 +573,14 @@ cudaError_t launch_act(const MxMaps &m, const MxGemmArgs &a, int num_sms, cudaSt
 // Short segments: with few rows a group the narrow form is ahead (128 experts, 1024 rows, K 4096, N 1536:
 // 81 us against 95).
 bool mx_gemm_narrow(const MxGemmArgs &a) { return a.filled <= (int64_t)64 * a.G; }
+
+cudaError_t mx_take_status(uint32_t *bits, cudaStream_t s) {
+    cudaError_t e = cudaMemcpyFromSymbolAsync(bits, g_unclaimed_status, sizeof *bits, 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess || !*bits) return e;
+    clear_status_kernel<<<1, 1, 0, s>>>(*bits);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_mx_gemm(const MxMaps &m, const MxGemmArgs &a, int format, int num_sms, cudaStream_t s) {
     const bool narrow = mx_gemm_narrow(a);

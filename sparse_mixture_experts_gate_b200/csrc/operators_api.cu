@@ -434,4 +434,18 @@ int moe_mx_gemm(const moe_mx_gemm_t *p, void *stream_v) {
     return launched(launch_mx_gemm(m, a, p->format, sms, as_stream(stream_v)), "moe_mx_gemm");
 }
 
+int moe_mx_status(void *stream_v) {
+    report_error(MOE_OK, "");
+    int sms = 0;
+    int rc = device_sms(&sms);
+    if (rc != MOE_OK) return rc;
+    uint32_t bits = 0;
+    if ((rc = launched(mx_take_status(&bits, as_stream(stream_v)), "moe_mx_status")) != MOE_OK) return rc;
+    if (bits & kDevTimeout)
+        return fail(MOE_ERR_TIMEOUT, "a bounded device-side wait of a product gave up (status 0x%x)", bits);
+    if (bits & kDevBadGroup)
+        return fail(MOE_ERR_INVALID_ARG, "a product's segment broke the bounds of its rows (status 0x%x)", bits);
+    return MOE_OK;
+}
+
 }  // extern "C"

@@ -161,7 +161,7 @@ def mx_gemm(a: MxTensor, w: MxTensor, group_start: Optional[torch.Tensor] = None
     + group_rows[g] of a (int32, starts multiples of 128), or all rows with one group and
     neither given. Rows of no group are left as they were in `out`, or hold anything where
     `out` is not given. status: an int32 tensor of one zero, whose bit 0 reports a wait that
-    gave up and bit 1 a segment outside the rows."""
+    gave up and bit 1 a segment outside the rows; without it `mx_status` tells of both."""
     if a.format != w.format or a.cols != w.cols:
         raise ValueError(f"operands differ: {a.format} of {a.cols} columns, {w.format} of {w.cols}")
     if a.groups != 1:
@@ -173,3 +173,11 @@ def mx_gemm(a: MxTensor, w: MxTensor, group_start: Optional[torch.Tensor] = None
     return _C.gemm(a.codes, a.scales, w.codes, w.scales, B.MOE_MX[a.format], a.rows, w.rows, a.cols, w.groups,
                    a.scale_exp + w.scale_exp, group_start, group_rows, bias, alpha, _ACT[activation], out,
                    dtype is torch.float32, status)
+
+
+def mx_status(device=None) -> None:
+    """Waits for the current stream of `device` (the current one) and raises MoEError if a product on it that
+    had no `status` gave up a wait (its output is incomplete) or skipped a segment outside its rows. Each
+    report comes once. Not while a graph is captured."""
+    with torch.cuda.device(device):
+        B.moe_mx_status(torch.cuda.current_stream().cuda_stream)

@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <utility>
 
 #include "moe.h"
 #include "moe_common.cuh"
@@ -53,6 +54,25 @@ bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % 
 bool overlap(const void *p, size_t np, const void *q, size_t nq) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
     return np && nq && a < b + nq && b < a + np;
+}
+
+// Whether two matrices of T rows of `width` bytes, lp and lq (at least `width`) apart, have a byte in common.
+// Rows between those of the other matrix (columns of one buffer) are none.
+bool rows_overlap(const void *p, int64_t lp, const void *q, int64_t lq, int64_t T, int64_t width) {
+    using wide = __int128;
+    wide a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    if (a < b) {
+        std::swap(a, b);
+        std::swap(lp, lq);
+    }
+    if (T <= 0 || a >= b + (wide)(T - 1) * lq + width) return false;
+    // Row i of the matrix that begins later lies behind row j of the other one. With the same stride i = 0 speaks for all.
+    for (int64_t i = 0; i < (lp == lq ? 1 : T); ++i) {
+        const wide from = a + (wide)i * lp - b, j = from / lq, off = from % lq;
+        if (j >= T) break;
+        if (off < width || (j + 1 < T && off + width > lq)) return true;
+    }
+    return false;
 }
 
 int launched(cudaError_t e, const char *what) {
@@ -226,6 +246,10 @@ int moe_route_backward(const moe_route_config_t *cfg, const float *grad_weights,
         return fail(MOE_ERR_INVALID_ARG, "grad_weights and topk_idx are required");
     if (!aligned(grad_weights, 4) || !aligned(topk_idx, 4))
         return fail(MOE_ERR_INVALID_ARG, "arrays must be 4-byte aligned");
+    const int64_t es = cfg->dtype == MOE_DTYPE_BF16 ? 2 : 4;
+    if (rows_overlap(logits, T == 1 ? cfg->num_experts * es : ld * es, grad_logits,
+                     T == 1 ? cfg->num_experts * es : grad_ld * es, T, cfg->num_experts * es))
+        return fail(MOE_ERR_INVALID_ARG, "grad_logits may not overlap logits");
     int sms = 0;
     if ((rc = device_sms(&sms)) != MOE_OK) return rc;
     RouteBackwardArgs a;

@@ -48,3 +48,21 @@ def test_skipped_segments_are_told_of_without_a_status_word():
         with pytest.raises(MoEError):
             ops.mx_status()
     ops.mx_status()
+
+
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_gradient_beside_its_logits(renormalize):
+    """Columns of one buffer, and rows that lie between the logits' rows, do not overlap; the logits themselves do."""
+    g = gen(2)
+    cfg = ops.RouteConfig(24, 3, renormalize=renormalize)
+    buf = torch.randn(40, 48, generator=g, device="cuda")
+    logits, plain = buf[:, :24], buf[:, :24].clone()
+    _, idx, _ = ops.route(plain, cfg)
+    gw = torch.randn(40, 3, generator=g, device="cuda")
+    want = ops.route_backward(gw, plain, idx, cfg)
+    assert torch.equal(ops.route_backward(gw, logits, idx, cfg, out=buf[:, 24:]), want)
+    assert torch.equal(logits, plain)
+    last = ops.route_backward(gw[39:], logits[39:], idx[39:], cfg, out=buf[38:39, :24])
+    assert torch.equal(last, want[39:])
+    with pytest.raises(MoEError, match="overlap"):
+        ops.route_backward(gw, plain, idx, cfg, out=plain)

@@ -477,7 +477,8 @@ MOE_API int moe_mx_quantize(int32_t format, const void *x, int32_t dtype, int64_
 
 /* moe_mx_quantize with a row_index (and without values) in another way: quantises every row of x once, into
  * `workspace` (>= moe_mx_once_bytes(format, x_rows, cols) bytes, 16-byte aligned), and copies the result to the
- * rows that want it. The same outputs; less work where rows are wanted three times or more.
+ * rows that want it. The same outputs, which may not overlap the workspace; less work where rows are wanted three
+ * times or more.
  * Errors: as there, and WORKSPACE. */
 MOE_API size_t moe_mx_once_bytes(int32_t format, int64_t x_rows, int64_t cols);
 MOE_API int moe_mx_quantize_once(int32_t format, const void *x, int32_t dtype, int64_t ld, int32_t x_rows, int32_t cols,

@@ -319,6 +319,10 @@ int moe_mx_quantize_once(int32_t format, const void *x, int32_t dtype, int64_t l
     if (ws_bytes < moe_mx_once_bytes(format, x_rows, cols))
         return fail(MOE_ERR_WORKSPACE, "workspace: %zu bytes given, %zu needed", ws_bytes,
                     moe_mx_once_bytes(format, x_rows, cols));
+    const size_t used = moe_mx_once_bytes(format, x_rows, cols);
+    if (overlap(workspace, used, codes, rows * (size_t)(cols / 2)) ||
+        overlap(workspace, used, scales, moe_mx_scales_bytes(format, rows, cols)))
+        return fail(MOE_ERR_INVALID_ARG, "the outputs may not overlap the workspace");
     if (rows == 0 || x_rows == 0) return MOE_OK;
     int sms = 0;
     if ((rc = device_sms(&sms)) != MOE_OK) return rc;

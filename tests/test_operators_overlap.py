@@ -30,3 +30,15 @@ def test_gradient_into_its_logits(L, dtype, es):
                            (-9 * es, 16, 9, 3), (4 * row, 8, 100, 5), (-100 * es + es, 100, 100, 2)):
         assert call(at, ld, gld, T) == B.MOE_ERR_INVALID_ARG, (at, ld, gld, T)
         assert b"overlap" in L.moe_last_error()
+
+
+def test_copies_into_the_workspace_of_rows_quantised_once(L):
+    """3 rows of 64: 36 bytes each in the workspace, 9 copies of 32 bytes of codes, one scale tile."""
+    def call(codes, scales, rows=9):
+        return L.moe_mx_quantize_once(0, P >> 4, 0, 64, 3, 64, P >> 4, rows, 0, codes, scales, P, 3 * 36, None)
+
+    far = P + (1 << 16)
+    for codes, scales in ((P, far), (P + 96, far), (P - 272, far), (far, P), (far, P + 96), (far, P - 496)):
+        assert call(codes, scales) == B.MOE_ERR_INVALID_ARG, (codes, scales)
+        assert b"overlap" in L.moe_last_error()
+    assert call(P, P, rows=0) == B.MOE_OK

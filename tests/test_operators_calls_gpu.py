@@ -66,3 +66,38 @@ def test_gradient_beside_its_logits(renormalize):
     assert torch.equal(last, want[39:])
     with pytest.raises(MoEError, match="overlap"):
         ops.route_backward(gw, plain, idx, cfg, out=plain)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_the_bindings_calls_are_the_operators(fmt):
+    """The ctypes functions on raw addresses, with the results that the tensors' functions have."""
+    g = gen(3)
+    f, s = B.MOE_MX[fmt], torch.cuda.current_stream().cuda_stream
+    logits = torch.randn(50, 40, generator=g, device="cuda")
+    cfg = ops.RouteConfig(40, 4, "sigmoid", 4, 2)
+    want = ops.route(logits, cfg)
+    w, idx, n = (torch.empty_like(t) for t in want)
+    B.moe_route(cfg.struct, logits.data_ptr(), 40, 50, None, w.data_ptr(), idx.data_ptr(), n.data_ptr(), s)
+    assert all(torch.equal(a, b) for a, b in zip((w, idx, n), want))
+    d = torch.empty_like(logits)
+    B.moe_route_backward(cfg.struct, w.data_ptr(), logits.data_ptr(), 40, idx.data_ptr(), 50, d.data_ptr(), 40, s)
+    assert torch.equal(d, ops.route_backward(w, logits, idx, cfg))
+
+    x, v = torch.randn(30, 96, generator=g, device="cuda"), torch.randn(20, 96, generator=g, device="cuda")
+    a, wq = ops.mx_quantize(x, fmt), ops.mx_quantize(v, fmt)
+    index = torch.randint(0, 30, (70,), generator=g, device="cuda", dtype=torch.int32)
+    codes = torch.zeros(70, 48, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(B.moe_mx_scales_bytes(f, 70, 96), dtype=torch.uint8, device="cuda")
+    B.moe_mx_gather(f, a.codes.data_ptr(), a.scales.data_ptr(), 30, 96, index.data_ptr(), 70, codes.data_ptr(),
+                    scales.data_ptr(), s)
+    q = ops.MxTensor(fmt, codes, scales, 70, 96)
+    assert torch.equal(codes, ops.mx_gather(a, index).codes)
+    val = torch.empty(70, 96, device="cuda")
+    B.moe_mx_dequantize(f, codes.data_ptr(), scales.data_ptr(), 70, 96, 0, val.data_ptr(), B.MOE_DTYPE["fp32"], 96, s)
+    assert torch.equal(val, ops.mx_dequantize(a)[index.long()])
+    out = torch.empty(70, 20, device="cuda")
+    B.moe_mx_gemm(B.MoeMxGemm(format=f, rows=70, n=20, k=96, groups=1, scale_exp=0, activation=B.MOE_ACT["gelu"],
+                              out_dtype=B.MOE_DTYPE["fp32"], out_ld=20, a_codes=codes.data_ptr(), a_scales=scales.data_ptr(),
+                              w_codes=wq.codes.data_ptr(), w_scales=wq.scales.data_ptr(), out=out.data_ptr()), s)
+    assert torch.equal(out, ops.mx_gemm(q, wq, activation="gelu", dtype=torch.float32))
+    B.moe_mx_status(s)

@@ -22,6 +22,7 @@
 // an MXFP4 one, whose scale it works out once; the lanes of 4 blocks put their
 // scale bytes together into the one 32-bit word that the scale tile holds of them.
 #include <algorithm>
+#include <cfloat>
 
 #include "mx_common.cuh"
 
@@ -187,20 +188,21 @@ template <int FMT, typename XT, bool PRE>
 __device__ __forceinline__ uint2 quantize16(const Raw<XT> &v, float pre, uint32_t &byte, float &scale) {
     uint32_t top = top_bits<XT>(v);
     if constexpr (FMT == kMxFp4) top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    // A finite maximum may leave the range when the power of two comes out: it then counts as infinite.
-    if (PRE) top = __float_as_uint(__uint_as_float(top) * pre);
     const bool finite = top < 0x7f800000u;
+    const float most = PRE ? __uint_as_float(top) * pre : __uint_as_float(top);
     float u[kLaneElems];
     if constexpr (FMT == kMxFp4) {
-        const int e = static_cast<int>(top >> 23) - 2;
+        int e = static_cast<int>(__float_as_uint(most) >> 23) - 2;
+        // Where 2^-e takes a finite maximum out of fp32's range its exponent is known all the same.
+        if (PRE && most == INFINITY) e = min(static_cast<int>((top >> 23) + (__float_as_uint(pre) >> 23)) - 129, 254);
         byte = finite ? static_cast<uint32_t>(e > 0 ? e : 0) : 255u;
         scale = e8m0_value(byte);
-        const float inv = __uint_as_float((254u - min(byte, 253u)) << 23);
+        const float inv = __uint_as_float(byte > 253u ? 1u << 22 : (254u - byte) << 23);
         // The scale first: what 2^-e alone would make too small for fp32's normal numbers keeps its digits.
 #pragma unroll
         for (int i = 0; i < kLaneElems; ++i) u[i] = PRE ? element<XT>(v, i) * inv * pre : element<XT>(v, i) * inv;
     } else {
-        byte = finite ? e4m3_of(__fdiv_rn(__uint_as_float(top), 6.f)) : 0u;
+        byte = finite ? e4m3_of(__fdiv_rn(PRE ? fminf(most, FLT_MAX) : most, 6.f)) : 0u;
         scale = e4m3_finite(byte);
         if constexpr (sizeof(XT) == 2) {
             const float inv = scale > 0.f ? rcp_approx(scale) : 0.f;

@@ -124,3 +124,21 @@ def test_values_of_the_largest_scales():
         q = ops.MxTensor("mxfp4", packed, ops.mx_tile_scales(byte), 1, 64, scale_exp=exp)
         want = ref.values(codes[None].cuda(), byte[0], "mxfp4", exp).float()
         assert torch.equal(ops.mx_dequantize(q), want)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_finite_numbers_that_an_exponent_takes_out_of_range(fmt, dtype):
+    """x 2^60 is finite where fp32 does not hold it: scales go to their largest, codes to 6; infinities stay NaN."""
+    x = torch.zeros(8, 64, dtype=dtype)
+    for r, v in enumerate((2.0 ** 67, 1.5 * 2.0 ** 68, 2.0 ** 69, 1.75 * 2.0 ** 69, 2.0 ** 70, -2.0 ** 100, torch.finfo(dtype).max,
+                           math.inf)):
+        x[r, 3], x[r, 7], x[r, 40] = v, -v / 4, 2.0 ** -61
+    x = x.cuda()
+    v = torch.empty_like(x)
+    q = ops.mx_quantize(x, fmt, scale_exp=-60, values=v)
+    codes, byte, want = ref.quantize(x, fmt, -60)
+    assert torch.equal(ref.scale_bytes(q.scales, 8, 64, fmt), byte)
+    assert torch.equal(ref.unpack(q.codes), codes)
+    assert torch.equal(v.double().nan_to_num(-7.0), want.nan_to_num(-7.0))
+    assert v[7, 3].isnan() and not v[:7].isnan().any()

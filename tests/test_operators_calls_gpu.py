@@ -101,3 +101,40 @@ def test_the_bindings_calls_are_the_operators(fmt):
                               w_codes=wq.codes.data_ptr(), w_scales=wq.scales.data_ptr(), out=out.data_ptr()), s)
     assert torch.equal(out, ops.mx_gemm(q, wq, activation="gelu", dtype=torch.float32))
     B.moe_mx_status(s)
+
+
+def test_calls_on_two_streams_at_once():
+    """Products of every form, quantisation with its workspace and routing, queued on two streams without waiting
+    for one another: each gives what it gives alone."""
+    g = gen(4)
+    cfg = ops.RouteConfig(256, 8, "sigmoid", 8, 4)
+    work = []
+    for fmt, rows, N, K, G in (("mxfp4", 2048, 512, 4096, 2), ("nvfp4", 2048, 512, 1024, 4), ("mxfp4", 1024, 640, 2048, 8)):
+        x = torch.randn(700, K, generator=g, device="cuda").bfloat16()
+        parts = [ops.mx_quantize(torch.randn(N, K, generator=g, device="cuda"), fmt) for _ in range(G)]
+        w = ops.MxTensor(fmt, torch.stack([p.codes for p in parts]), torch.stack([p.scales for p in parts]), N, K, groups=G)
+        index = torch.randint(0, 700, (rows * 2,), generator=g, device="cuda", dtype=torch.int32)
+        start = (torch.arange(G, device="cuda") * (rows // G)).to(torch.int32)
+        count = torch.full((G,), 9 if rows == 1024 else rows // G, dtype=torch.int32, device="cuda")
+        logits = torch.randn(500, 256, generator=g, device="cuda")
+        work.append((fmt, x, index, w, start, count, logits))
+
+    def step(i):
+        fmt, x, index, w, start, count, logits = work[i % len(work)]
+        q = ops.mx_quantize(x, fmt, row_index=index)
+        y = ops.mx_gemm(q, w, start, count, out=torch.zeros(index.numel(), w.rows, dtype=torch.bfloat16, device="cuda"))
+        wts, idx, n = ops.route(logits, cfg)
+        return y, wts, idx, n, ops.route_backward(wts, logits, idx, cfg)
+
+    want = [step(i) for i in range(3)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for i in range(30):
+        for j, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append((i + j, step(i + j)))
+    torch.cuda.synchronize()
+    for i, outs in got:
+        assert all(torch.equal(a, b) for a, b in zip(outs, want[i % 3]))
+    ops.mx_status()

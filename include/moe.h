@@ -512,13 +512,14 @@ MOE_API int moe_mx_dequantize(int32_t format, const void *codes, const void *sca
  *                      Other rows of out are left as they were. A segment that
  *                      breaks these bounds is not computed, and sets bit 1 of *status
  *   bias               [groups][n] fp32 or NULL; alpha [groups] fp32 or NULL (1)
- *   scale_exp          -120..120, the sum of both operands' exponents
+ *   scale_exp          -120..120, the sum of both operands' exponents; alpha[g] 2^scale_exp
+ *                      is one factor in fp32, and has to be a normal number there (or 0)
  *   activation         MOE_ACT_*, MOE_ACT_NONE = none
  *   out                rows of n, out_ld apart, out_dtype MOE_DTYPE_*
  *   status             device word: bits are or-ed in (bit 0: a bounded wait gave up,
  *                      out is incomplete; bit 1 as above). NULL: moe_mx_status tells
  * groups <= 1024, groups x n < 2^31 - 1024, and groups (rows / 192 + 1) n / 256 (short
- * segments, rows < 192 groups: / 64 and / 128) below about 2^31. rows = 0 enqueues nothing. Needs no
+ * segments, rows <= 191 groups, or 64 with one group: / 64 and / 128) below about 2^31. rows = 0 enqueues nothing. Needs no
  * workspace; calls on any streams may overlap. Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 typedef struct {
     int32_t format, rows, n, k, groups;

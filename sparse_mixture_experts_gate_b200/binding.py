@@ -468,8 +468,9 @@ class MoELayer:
         moe_prepare_router(self.handle, self._planes.data_ptr(), self._planes.numel(), s)
 
     def set_routing(self, cfg):
-        """Route as an operators.RouteConfig says (moe_set_routing); None returns to
-        the router's own selection."""
+        """Route the forwards from now on as an operators.RouteConfig says (moe_set_routing);
+        None returns to the router's own selection. StepGraphs and HostPipelines made before
+        it keep the routing they were captured with."""
         moe_set_routing(self.handle, None if cfg is None else cfg.struct)
 
     def prepare_experts_mx(self, fmt: Optional[str] = "mxfp4", w1_exp: Optional[int] = None,

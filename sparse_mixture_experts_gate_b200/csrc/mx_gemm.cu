@@ -571,7 +571,9 @@ cudaError_t launch_act(const MxMaps &m, const MxGemmArgs &a, int num_sms, cudaSt
 }  // namespace
 
 // Short segments: with few rows a group the narrow form is ahead (128 experts, 1024 rows, K 4096, N 1536:
-// 81 us against 95).
+// 81 us against 95). The border is one of its tiles for each group; between 8 rows a group and that the two
+// were not compared. `filled` is a lower bound where there are several groups: segments that leave little unused
+// count as fewer rows than they have.
 bool mx_gemm_narrow(const MxGemmArgs &a) { return a.filled <= (int64_t)64 * a.G; }
 
 cudaError_t mx_take_status(uint32_t *bits, cudaStream_t s) {
@@ -586,7 +588,8 @@ cudaError_t launch_mx_gemm(const MxMaps &m, const MxGemmArgs &a, int format, int
     const bool narrow = mx_gemm_narrow(a);
     // Both accumulators a unit from K = 4096 on: 218 us instead of 251 at K = 7168 (32 experts, 32768
     // rows, N 2048, MXFP4), where the epilogue is short beside the products; 123 instead of 113 at K = 2048
-    // (64 experts, 49152 rows, N 1408, NVFP4).
+    // (64 experts, 49152 rows, N 1408, NVFP4). Between the two the border was not measured, nor with segments of
+    // at most 192 rows, which leave the second accumulator empty.
     const bool deep = a.K >= 4096;
     if (format == kMxFp4)
         return narrow ? launch_act<kMxFp4, 64, 1, 1>(m, a, num_sms, s)

@@ -390,8 +390,8 @@ bool vector_rows(const void *p, int64_t ld, int elem, int bytes) {
 template <int FMT, typename XT, int STEPS>
 cudaError_t quantize(const MxQuantArgs &a, int num_sms, cudaStream_t s) {
     const int64_t items = (int64_t)a.rows * ((a.cols + kStep * STEPS - 1) / (kStep * STEPS));
-    // Rows per block: one piece for each warp, and no more blocks than 64 for each SM. An index far longer
-    // than x has mostly rows that are none: 8 rows a block (one token in 16256 rows x 4096 4 us, 6 with 4;
+    // Rows per block: one piece for each warp, and more (up to 32) where there would be more than 64 blocks for
+    // each SM. An index far longer than x has mostly rows that are none: 8 rows a block (one token in 16256 rows x 4096 4 us, 6 with 4;
     // 128 tokens in 17280, some blocks full, 8 us, 10 with 16).
     int rpb = 1;
     while (rpb < 32 && ((int64_t)rpb * items < (int64_t)a.rows * (kThreads / 32) || a.rows / rpb > 64 * num_sms)) rpb *= 2;

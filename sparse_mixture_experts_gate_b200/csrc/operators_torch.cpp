@@ -167,7 +167,8 @@ py::tuple quantize(const Tensor &x, int format, const Maybe &row_index, int scal
         // Rows that are wanted several times are quantised once and copied: 8192 x 2048 NVFP4 to six times as many
         // rows 27 us, 49 without, 32768 x 7168 MXFP4 to three times 210 and 254; to twice as many it is little or no
         // gain (170 and 172). Below this size it is not worth the launch (1024 x 2048 to 6144 rows 8 and 10 us, 256 x
-        // 7168 to 2048 12 and 10). Many rows of the index may be none: the rows of x are what is sure.
+        // 7168 to 2048 12 and 10). The index's length counts: it may have many rows that are none (padded segments),
+        // and how many only the device knows.
         const int64_t bytes = static_cast<int64_t>(moe_mx_once_bytes(format, x_rows, cols));
         const Tensor workspace = empty({bytes}, at::kByte, x);
         check(moe_mx_quantize_once(format, x.data_ptr(), type, ld, nx, nc, index, n, scale_exp, codes.data_ptr(),

@@ -537,8 +537,9 @@ __global__ void __launch_bounds__(kThreads, RE > 8 ? 2 : 3) route_kernel(const _
 // twice adds up (in the order of the choices). Lane l writes (DENSE: also reads)
 // experts 4 l .. 4 l + 3 of every 128 in one access where the rows allow it.
 //
-// Bound by HBM where T E is large: the row is written once and read only where every
-// logit has a gradient (the softmax that is not renormalised).
+// The row is written once and read only where every logit has a gradient (the softmax that is
+// not renormalised): 32768 x 256 fp32 in 14.4 us then, 16.4 in a loop of calls (4.2 to 4.8 TB/s, the issue slots
+// 68% taken: both are near), 9.1 for the renormalised sigmoid.
 template <typename XT, int N>
 struct alignas(N * sizeof(XT)) Pack {
     XT v[N];

@@ -48,13 +48,15 @@ def route(logits: torch.Tensor, cfg: RouteConfig, bias: Optional[torch.Tensor] =
           out=(None, None, None)) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
     """Routes the tokens of logits [T][E] (bf16 or fp32). Returns (weights [T][k] fp32,
     topk_idx [T][k] int32, selections per expert [E] int32 or None); `out`: these
-    three to write into. bias [E] fp32 takes part in the selection only."""
+    three to write into, the last one None for no counts (`counts` says whether they are
+    made where `out` is not given). bias [E] fp32 takes part in the selection only."""
     return _C.route(logits, cfg._at, bias, counts, *out)
 
 
 def route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, topk_idx: torch.Tensor, cfg: RouteConfig,
                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """The gradient with respect to logits, given that of route's weights [T][k] fp32."""
+    """The gradient with respect to logits, given that of route's weights [T][k] fp32. `out` may
+    not overlap logits."""
     return _C.route_backward(grad_weights, logits, topk_idx, cfg._at, out)
 
 
